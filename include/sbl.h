@@ -337,6 +337,143 @@ size_t sbl_backward_workspace_bytes(int64_t t, int64_t k, uint32_t flags);
 sbl_status sbl_backward_ws(const sbl_layer* layer, const void* x, const void* dy, int64_t t, void* dx, void* dw,
                            uint32_t flags, void* workspace, sbl_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the products: the operators that a training or serving step runs
+ * between sbl_forward / sbl_backward calls.  The paper has no counterpart for
+ * them beyond naming the network they sit in.  Same conventions as above
+ * (device pointers, caller-owned buffers, no synchronisation, capturable into
+ * CUDA graphs).  `status_dev` is a caller-owned device uint32 or NULL (then
+ * device-side errors are not reported).
+ * ------------------------------------------------------------------------- */
+
+/* Types of the operands of sbl_rmsnorm_forward / sbl_rmsnorm_backward; a
+ * clear bit means bf16. */
+enum {
+  SBL_NORM_X_F32 = 1u << 0,      /* x is fp32 (e.g. a linear's y) */
+  SBL_NORM_STREAM_F32 = 1u << 1, /* the residual stream is fp32: residual, h, dres, dh */
+  SBL_NORM_W_F32 = 1u << 2,      /* weight is fp32 */
+  SBL_NORM_DY_F32 = 1u << 3      /* the incoming gradients are fp32 */
+};
+
+#define SBL_NORM_MAX_K 16384
+
+/* Root-mean-square norm of t rows of k elements, with the residual's addition
+ * in front and the activation quantisation behind it, in one pass:
+ *   h    = RN(x + residual), rounded to the stream's type; h = x without a residual
+ *   rstd = RN_fp32(1 / sqrt(mean_k h^2 + eps)), the mean in fp64
+ *   xn   = RN_bf16(RN_fp32(RN_fp32(h rstd) weight)); weight NULL: 1
+ *   xscale, xq = the codes that sbl_quantize_activations gives for xn, bit for bit
+ *   xhat = RN_bf16(xq xscale / 127), the dW operand of SBL_DW_QUANT_X
+ * x, residual: [t, k]; weight: [k].  Outputs, each may be NULL, one at least
+ * is wanted: h_out [t, k] (the stream's type; without a residual x's type),
+ * xn_out and xhat_out bf16 [t, k], xq_out int8 [t, k], xscale_out fp32 [t],
+ * rstd_out fp32 [t].  h_out may be `residual`; no other overlap of an output
+ * with another argument.  k: a multiple of 8 up to SBL_NORM_MAX_K (of 64 when
+ * the codes are to enter sbl_forward_quantized); eps: 1e-12 to 1.  A row of
+ * zeros gives xn = 0, xscale = 1e-5, xq = 0.  A non-finite h or xn raises
+ * SBL_STATUS_NONFINITE_X; the other rows are not touched by it.  t == 0 is a
+ * no-op. */
+sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* weight, int64_t t, int64_t k,
+                               double eps, uint32_t flags, void* h_out, void* xn_out, void* xhat_out, int8_t* xq_out,
+                               float* xscale_out, float* rstd_out, uint32_t* status_dev, sbl_stream_t stream);
+
+/* Backward of the above, straight through the quantiser.  dys: `dy_count`
+ * (1 to 3) pointers to gradients [t, k] of xn, which are added (the dX of the
+ * products that share the input: q, k and v; gate and up); dres [t, k] (NULL:
+ * zero) the gradient that reaches h along the residual stream.
+ *   g   = sum dys,  n = h rstd
+ *   dh  = dres + rstd (weight g - n mean_k(weight g n))   [t, k], the stream's type
+ *   dx  = RN_bf16 of the same value, optional (the dy that sbl_backward of the
+ *         linear in front takes when the stream is fp32)
+ *   dw  = sum_t g n   fp32 [k], optional
+ * dh is the gradient of x and of residual alike.  h is the forward's h_out (or
+ * its x, without a residual) in the stream's type.  dh may be dres.  dw needs
+ * `workspace`, sbl_rmsnorm_backward_workspace_bytes(t, k) bytes, 16-byte
+ * aligned; its sum has a fixed order.  t == 0: dw = 0. */
+sbl_status sbl_rmsnorm_backward(const void* h, const float* rstd, const void* weight, const void* const* dys,
+                                int32_t dy_count, const void* dres, int64_t t, int64_t k, uint32_t flags, void* dh,
+                                void* dx, float* dw, void* workspace, sbl_stream_t stream);
+size_t sbl_rmsnorm_backward_workspace_bytes(int64_t t, int64_t k);
+
+/* Flags of sbl_adamw_tensor.flags. */
+enum {
+  SBL_ADAMW_GRAD_F32 = 1u << 0,   /* grad is fp32 instead of bf16 */
+  SBL_ADAMW_STATE_8BIT = 1u << 1, /* m and v hold 8 bits an element */
+  SBL_ADAMW_NO_DECAY = 1u << 2    /* no weight decay for this tensor */
+};
+#define SBL_ADAMW_BLOCK 256 /* elements that share a scale in the 8-bit states */
+
+/* One tensor of an AdamW step, dense, numel elements. */
+typedef struct sbl_adamw_tensor {
+  void* w;          /* bf16 weights (the masters that sbl_prepare_weights reads), updated */
+  float* master;    /* fp32 copy that holds the weights' exact value, updated; NULL: w itself is the value */
+  const void* grad; /* gradient (sbl_backward's dw) */
+  void* m;          /* first moment: fp32, or e4m3 with SBL_ADAMW_STATE_8BIT */
+  void* v;          /* second moment: fp32, or e4m3 of its square root */
+  float* m_scale;   /* 8-bit only: one per SBL_ADAMW_BLOCK elements, ceil(numel / 256) of them */
+  float* v_scale;
+  int64_t numel;
+  uint32_t flags;
+  uint32_t reserved; /* 0 */
+} sbl_adamw_tensor;
+
+typedef struct sbl_adamw_params {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;            /* 1 for the first step */
+  const float* lr_dev;     /* device scalars for captured graphs, each may be NULL: used instead of lr, */
+  const int64_t* step_dev; /* instead of step, */
+  const float* grad_scale_dev; /* and the factor on every gradient (clipping, loss scale); NULL: 1 */
+} sbl_adamw_params;
+
+/* One AdamW step on `count` tensors (any number; up to 128 go in one launch):
+ *   g = grad grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   value -= lr weight_decay value;  value -= lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *   w = RN_bf16(value), value in `master` (or in w)
+ * in fp32.  8-bit states: per block of 256 elements m = code m_scale and
+ * sqrt(v) = code v_scale with e4m3 codes (float8_e4m3fn), the scale the
+ * block's largest magnitude / 448; codes round to nearest, except that a
+ * second moment above zero never becomes zero.  A block whose largest
+ * magnitude is below 2^-100 holds zeros with scale 0.  The step itself uses
+ * m and v before that rounding.  Nearest rounding moves a code only when its
+ * value changes by about 3 to 6 %: use beta2 of 0.95 or so with 8-bit states, not
+ * 0.999.  Zeroed states (scales too) are the start.  Tensors of a call must
+ * not share memory (two entries with the same w: SBL_ERR_INVALID_ARG).
+ * Alignment: w, master, grad, m and v 16 bytes, the scales 4.  A non-finite
+ * gradient raises SBL_STATUS_NONFINITE_G; that tensor's block of 256 is then
+ * unspecified.  numel 0 and count 0 are no-ops.  SBL_ERR_SHAPE: negative
+ * numel or one above 2^40; SBL_ERR_INVALID_ARG: step < 1 (without step_dev),
+ * a beta outside [0, 1), eps, lr or weight_decay negative or not finite. */
+sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const sbl_adamw_params* params,
+                          uint32_t* status_dev, sbl_stream_t stream);
+
+/* Softmax cross entropy of a linear head, without its logits in memory:
+ *   z = h w^T,  lse_i = log sum_j exp z_ij,  loss_i = lse_i - z_i,target_i
+ * h: bf16 [t, d]; w: bf16 [v, d]; targets: int64 [t], `ignore_index` for rows
+ * without loss (loss 0; lse is still written).  loss, lse: fp32 [t].  d: a
+ * multiple of 8 up to 131072; v >= 1 and t up to 2^22.  A target outside
+ * [0, v) that is not ignore_index gives loss NaN and raises
+ * SBL_STATUS_BAD_TARGET.  targets, loss, lse and dloss need only their
+ * elements' own alignment.  `workspace`: sbl_linear_ce_workspace_bytes(t, v, d,
+ * 0) bytes, 256-byte aligned.  t == 0 is a no-op. */
+sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* targets, int64_t t, int64_t v, int64_t d,
+                                 int64_t ignore_index, float* loss, float* lse, void* workspace, uint32_t* status_dev,
+                                 sbl_stream_t stream);
+
+/* Its backward pass from the forward's lse.  dloss: fp32, the gradient of each
+ * row's loss, dloss[i * dloss_stride] (stride 0: one value for all rows).
+ *   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]), 0 for ignored rows and rows with a bad target
+ *   dh = dz w  bf16 [t, d],   dw = dz^T h  bf16 [v, d]
+ * The logits are computed again, a piece of the vocabulary at a time; dz is
+ * rounded to bf16 for the two products, which accumulate in fp32.
+ * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 1) bytes, 256-byte
+ * aligned.  t == 0: dw = 0. */
+sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,
+                                  const float* dloss, int64_t dloss_stride, int64_t t, int64_t v, int64_t d,
+                                  int64_t ignore_index, void* dh, void* dw, void* workspace, uint32_t* status_dev,
+                                  sbl_stream_t stream);
+/* 0 for sizes the calls refuse. */
+size_t sbl_linear_ce_workspace_bytes(int64_t t, int64_t v, int64_t d, int32_t backward);
+
 /* Synchronises `stream`, then maps the layer's device status word to a code:
  * SBL_OK, SBL_ERR_NONFINITE or SBL_ERR_TIMEOUT.  *bits_out (may be NULL)
  * receives the raw word.  The word stays set until sbl_clear_status or the
@@ -386,7 +523,9 @@ sbl_status sbl_selftest_mma_rate(int32_t kind, int32_t stages, int32_t pairs, ui
 enum {
   SBL_STATUS_NONFINITE_W = 1u << 0,
   SBL_STATUS_NONFINITE_X = 1u << 1,
-  SBL_STATUS_TIMEOUT = 1u << 2
+  SBL_STATUS_TIMEOUT = 1u << 2,
+  SBL_STATUS_NONFINITE_G = 1u << 3, /* sbl_adamw_step: a non-finite gradient */
+  SBL_STATUS_BAD_TARGET = 1u << 4   /* sbl_linear_ce_*: a target outside [0, v) */
 };
 
 /* Library version string. */

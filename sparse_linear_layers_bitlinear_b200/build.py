@@ -42,7 +42,7 @@ def _stale() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
-    cmd = [_nvcc(), *NVCC_FLAGS, "-shared", "-o", LIB, *sources()]
+    cmd = [_nvcc(), *NVCC_FLAGS, "--threads", "0", "-shared", "-o", LIB, *sources()]
     if verbose:
         cmd.insert(1, "-Xptxas")
         cmd.insert(2, "-v")

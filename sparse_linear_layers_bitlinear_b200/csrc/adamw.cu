@@ -1,0 +1,326 @@
+// AdamW over many tensors in one launch, states in fp32 or in 8 bits.
+//
+//   g = grad scale,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   value = value (1 - lr wd) - lr (m / c1) / (sqrt(v / c2) + eps),  c = 1 - b^step
+//
+// Elementwise: bound by the bytes of the states and weights (28 a weight with
+// fp32 states, master and a bf16 gradient; 16 with 8-bit states).  The tensors'
+// addresses travel as kernel parameters, so a launch needs no device table and
+// can be captured; a block finds its tensor by its chunk's number.
+//
+// 8-bit states: a warp holds a block of 256 elements, 8 a lane, so the block's
+// largest magnitude is one warp reduction.  A value is e4m3 code times scale,
+// the second moment through its square root, which halves the exponent range
+// it needs.  Nearest rounding, half a step 2^-4 relative; the second moment
+// never rounds to zero (the smallest code stands in), since a zero would let
+// the next step divide by eps.
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "sbl_device.cuh"
+#include "sbl_kernels.h"
+
+namespace sbl {
+
+namespace {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamChunk = 4096;  // elements of one tensor that a block updates
+constexpr float kFlush = 0x1p-100f;
+constexpr float kFp8Max = 448.0f, kFp8Min = 0x1p-9f;
+
+struct AdamEntry {
+  void* w;
+  float* master;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t numel;
+  uint32_t flags;
+};
+
+struct AdamLaunch {
+  AdamEntry entry[kAdamMaxTensors];
+  uint32_t first[kAdamMaxTensors + 1];  // first chunk of each tensor
+  int count;
+  float lr, b1, one_b1, b2, one_b2, eps, decay;
+  float c1, c2;          // 1 - beta^step
+  double log_b1, log_b2; // for step_dev
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* grad_scale_dev;
+  uint32_t* status;
+};
+
+// The step's scalars.
+struct AdamStep {
+  float b1, one_b1, b2, one_b2, eps;
+  float keep;      // 1 - lr decay
+  float rate;      // lr / c1
+  float inv_root;  // 1 / sqrt(c2)
+  float scale;     // of the gradients
+};
+
+__device__ __forceinline__ AdamStep adam_step(const AdamLaunch& p, bool no_decay) {
+  AdamStep s;
+  s.b1 = p.b1, s.one_b1 = p.one_b1, s.b2 = p.b2, s.one_b2 = p.one_b2, s.eps = p.eps;
+  const float lr = p.lr_dev != nullptr ? *p.lr_dev : p.lr;
+  float c1 = p.c1, c2 = p.c2;
+  if (p.step_dev != nullptr) {
+    const double n = static_cast<double>(*p.step_dev);
+    c1 = static_cast<float>(-expm1(n * p.log_b1));
+    c2 = static_cast<float>(-expm1(n * p.log_b2));
+  }
+  s.keep = no_decay ? 1.0f : 1.0f - lr * p.decay;
+  s.rate = lr / c1;
+  s.inv_root = 1.0f / sqrtf(c2);
+  s.scale = p.grad_scale_dev != nullptr ? *p.grad_scale_dev : 1.0f;
+  return s;
+}
+
+// One element; m, v and value are updated.
+__device__ __forceinline__ void adam_element(const AdamStep& s, float grad, float& m, float& v, float& value,
+                                             bool& bad) {
+  const float g = grad * s.scale;
+  bad |= !(fabsf(g) <= 3.402823466e38f);
+  m = fmaf(s.b1, m, s.one_b1 * g);
+  v = fmaf(s.b2, v, s.one_b2 * g * g);
+  const float den = fmaf(sqrtf(v), s.inv_root, s.eps);
+  value = fmaf(value, s.keep, -(s.rate * m) / den);
+}
+
+template <bool F32>
+__device__ __forceinline__ void load4(const void* base, int64_t i, float (&f)[4]) {
+  if constexpr (F32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+  } else {
+    const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+    f[0] = __uint_as_float(a.x << 16), f[1] = __uint_as_float(a.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(a.y << 16), f[3] = __uint_as_float(a.y & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ float load1(const void* base, int64_t i, bool f32) {
+  if (f32) return static_cast<const float*>(base)[i];
+  return __uint_as_float(uint32_t(static_cast<const uint16_t*>(base)[i]) << 16);
+}
+
+__device__ __forceinline__ void store4(float* base, int64_t i, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(base + i) = make_float4(f[0], f[1], f[2], f[3]);
+}
+
+__device__ __forceinline__ void store4_bf16(void* base, int64_t i, const float (&f)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Four e4m3 codes of a word.
+__device__ __forceinline__ void from_fp8(uint32_t word, float (&f)[4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(word >> (16 * h)), __NV_E4M3);
+    const float2 v = __half22float2(__half2(raw));
+    f[2 * h] = v.x, f[2 * h + 1] = v.y;
+  }
+}
+
+__device__ __forceinline__ uint32_t to_fp8(const float (&f)[4]) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+template <bool GF32, bool MASTER>
+__device__ __forceinline__ void update_fp32(const AdamEntry& t, const AdamStep& s, int64_t first, bool& bad) {
+  constexpr int U = kAdamChunk / (4 * kAdamThreads);
+  float* mp = static_cast<float*>(t.m);
+  float* vp = static_cast<float*>(t.v);
+  const int64_t at = first + 4 * threadIdx.x;
+  if (first + kAdamChunk <= t.numel) {
+    float g[U][4], m[U][4], v[U][4], x[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = at + u * 4 * kAdamThreads;
+      load4<GF32>(t.grad, i, g[u]);
+      load4<true>(mp, i, m[u]);
+      load4<true>(vp, i, v[u]);
+      load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = at + u * 4 * kAdamThreads;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) adam_element(s, g[u][e], m[u][e], v[u][e], x[u][e], bad);
+      store4(mp, i, m[u]);
+      store4(vp, i, v[u]);
+      if (MASTER) store4(t.master, i, x[u]);
+      store4_bf16(t.w, i, x[u]);
+    }
+    return;
+  }
+  for (int64_t i = first + threadIdx.x; i < t.numel; i += kAdamThreads) {
+    float x = MASTER ? t.master[i] : load1(t.w, i, false), m = mp[i], v = vp[i];
+    adam_element(s, load1(t.grad, i, GF32), m, v, x, bad);
+    mp[i] = m;
+    vp[i] = v;
+    if (MASTER) t.master[i] = x;
+    static_cast<__nv_bfloat16*>(t.w)[i] = __float2bfloat16_rn(x);
+  }
+}
+
+// Largest magnitude of the warp's values (their bits order as the values do).
+__device__ __forceinline__ float warp_top(float top) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+}
+
+// A block of 256 elements by one warp: lane l holds elements 4 l .. 4 l + 3
+// and 128 more on.
+template <bool GF32, bool MASTER>
+__device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s, int64_t first, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* mp = static_cast<uint8_t*>(t.m);
+  uint8_t* vp = static_cast<uint8_t*>(t.v);
+  for (int b = threadIdx.x >> 5; b < kAdamChunk / SBL_ADAMW_BLOCK; b += kAdamThreads / 32) {
+    const int64_t start = first + b * SBL_ADAMW_BLOCK;
+    if (start >= t.numel) return;
+    const int64_t block = start / SBL_ADAMW_BLOCK;
+    const float ms = t.m_scale[block], vs = t.v_scale[block];
+    float g[2][4], m[2][4], v[2][4], x[2][4];
+    const bool full = start + SBL_ADAMW_BLOCK <= t.numel;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t i = start + 128 * h + 4 * lane;
+      if (full) {
+        load4<GF32>(t.grad, i, g[h]);
+        load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i, x[h]);
+        from_fp8(*reinterpret_cast<const uint32_t*>(mp + i), m[h]);
+        from_fp8(*reinterpret_cast<const uint32_t*>(vp + i), v[h]);
+      } else {
+        uint32_t mw = 0, vw = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool in = i + e < t.numel;
+          g[h][e] = in ? load1(t.grad, i + e, GF32) : 0.0f;
+          x[h][e] = in ? (MASTER ? t.master[i + e] : load1(t.w, i + e, false)) : 0.0f;
+          if (in) {
+            mw |= uint32_t(mp[i + e]) << (8 * e);
+            vw |= uint32_t(vp[i + e]) << (8 * e);
+          }
+        }
+        from_fp8(mw, m[h]);
+        from_fp8(vw, v[h]);
+      }
+    }
+    float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m[h][e] *= ms;
+        v[h][e] *= vs;
+        v[h][e] *= v[h][e];
+        adam_element(s, g[h][e], m[h][e], v[h][e], x[h][e], bad);
+        v[h][e] = sqrtf(v[h][e]);
+        mtop = fmaxf(mtop, fabsf(m[h][e]));
+        vtop = fmaxf(vtop, v[h][e]);
+      }
+    mtop = warp_top(mtop);
+    vtop = warp_top(vtop);
+    const float mi = mtop >= kFlush ? kFp8Max / mtop : 0.0f, vi = vtop >= kFlush ? kFp8Max / vtop : 0.0f;
+    if (lane == 0) {
+      t.m_scale[block] = mtop >= kFlush ? mtop / kFp8Max : 0.0f;
+      t.v_scale[block] = vtop >= kFlush ? vtop / kFp8Max : 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t i = start + 128 * h + 4 * lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        m[h][e] *= mi;
+        v[h][e] *= vi;
+        if (v[h][e] > 0.0f) v[h][e] = fmaxf(v[h][e], kFp8Min);
+      }
+      const uint32_t mw = to_fp8(m[h]), vw = to_fp8(v[h]);
+      if (full) {
+        *reinterpret_cast<uint32_t*>(mp + i) = mw;
+        *reinterpret_cast<uint32_t*>(vp + i) = vw;
+        if (MASTER) store4(t.master, i, x[h]);
+        store4_bf16(t.w, i, x[h]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (i + e >= t.numel) break;
+          mp[i + e] = static_cast<uint8_t>(mw >> (8 * e));
+          vp[i + e] = static_cast<uint8_t>(vw >> (8 * e));
+          if (MASTER) t.master[i + e] = x[h][e];
+          static_cast<__nv_bfloat16*>(t.w)[i + e] = __float2bfloat16_rn(x[h][e]);
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamLaunch p) {
+  int lo = 0, hi = p.count - 1;  // the last tensor whose first chunk is not past this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.first[mid] <= blockIdx.x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const AdamEntry t = p.entry[lo];
+  const int64_t first = int64_t(blockIdx.x - p.first[lo]) * kAdamChunk;
+  pdl_wait();
+  pdl_trigger();
+  const AdamStep s = adam_step(p, (t.flags & SBL_ADAMW_NO_DECAY) != 0u);
+  bool bad = false;
+  const bool gf = (t.flags & SBL_ADAMW_GRAD_F32) != 0u, master = t.master != nullptr;
+  if (t.flags & SBL_ADAMW_STATE_8BIT) {
+    if (gf)
+      master ? update_fp8<true, true>(t, s, first, bad) : update_fp8<true, false>(t, s, first, bad);
+    else
+      master ? update_fp8<false, true>(t, s, first, bad) : update_fp8<false, false>(t, s, first, bad);
+  } else {
+    if (gf)
+      master ? update_fp32<true, true>(t, s, first, bad) : update_fp32<true, false>(t, s, first, bad);
+    else
+      master ? update_fp32<false, true>(t, s, first, bad) : update_fp32<false, false>(t, s, first, bad);
+  }
+  if (bad) raise_status(p.status, SBL_STATUS_NONFINITE_G);
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const sbl_adamw_tensor* tensors, int count, const sbl_adamw_params& q, uint32_t* status,
+                         cudaStream_t s) {
+  if (count < 1 || count > kAdamMaxTensors) return cudaErrorInvalidValue;
+  AdamLaunch p = {};
+  uint64_t chunks = 0;
+  for (int i = 0; i < count; ++i) {
+    const sbl_adamw_tensor& t = tensors[i];
+    p.entry[i] = AdamEntry{t.w, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.numel, t.flags};
+    p.first[i] = static_cast<uint32_t>(chunks);
+    chunks += (uint64_t(t.numel) + kAdamChunk - 1) / kAdamChunk;
+    if (chunks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  }
+  p.first[count] = static_cast<uint32_t>(chunks);
+  p.count = count;
+  p.lr = static_cast<float>(q.lr);
+  p.b1 = static_cast<float>(q.beta1), p.one_b1 = static_cast<float>(1.0 - q.beta1);
+  p.b2 = static_cast<float>(q.beta2), p.one_b2 = static_cast<float>(1.0 - q.beta2);
+  p.eps = static_cast<float>(q.eps), p.decay = static_cast<float>(q.weight_decay);
+  p.log_b1 = std::log(q.beta1), p.log_b2 = std::log(q.beta2);
+  p.c1 = static_cast<float>(1.0 - std::pow(q.beta1, double(q.step)));
+  p.c2 = static_cast<float>(1.0 - std::pow(q.beta2, double(q.step)));
+  p.lr_dev = q.lr_dev, p.step_dev = q.step_dev, p.grad_scale_dev = q.grad_scale_dev;
+  p.status = status;
+  return launch_pdl(k_adamw, dim3(static_cast<unsigned>(chunks)), dim3(kAdamThreads), 0, s, p);
+}
+
+}  // namespace sbl

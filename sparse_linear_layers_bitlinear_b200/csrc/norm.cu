@@ -1,0 +1,478 @@
+// Root-mean-square norm with the residual's addition in front and the int8
+// activation quantisation behind it, and its backward pass.
+//
+// Forward, one row of k elements:
+//   h = RN(x + r),  rstd = RN_fp32(1 / sqrt(mean h^2 + eps)),
+//   xn = RN_bf16(RN_fp32(RN_fp32(h rstd) w)),  then the act-quant of xn.
+// The row stays in registers between its three uses (the sum of squares, the
+// row maximum, the codes), so every operand crosses HBM once.  The squares
+// are added in fp64: the result is then the same for every split of the row,
+// and rstd is the correctly rounded value but for about one row in 10^7, so
+// the int8 codes, which sit behind two roundings, are reproducible.
+//
+// A row belongs to a group of TPR threads, R vectors of 8 elements a thread.
+#include <cuda_bf16.h>
+
+#include "actq_math.cuh"
+#include "sbl_device.cuh"
+#include "sbl_kernels.h"
+
+namespace sbl {
+
+namespace {
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t vec, float (&f)[8]) {
+  if constexpr (F32) {
+    const float4* src = static_cast<const float4*>(base) + 2 * vec;
+    const float4 a = src[0], b = src[1];
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    const uint4 a = static_cast<const uint4*>(base)[vec];
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(u[e] << 16);
+      f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* base, int64_t vec, const float (&f)[8]) {
+  if constexpr (F32) {
+    float4* dst = static_cast<float4*>(base) + 2 * vec;
+    dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+    dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    static_cast<uint4*>(base)[vec] = pack8(f);
+  }
+}
+
+// RN_fp32(1 / sqrt(a)): the fp32 reciprocal root and two Newton steps in fp64
+// (relative error far below fp64's 2^-53 of the exact step), one rounding.
+__device__ __forceinline__ float inverse_root(double a) {
+  if (!(a < 1e37)) return static_cast<float>(1.0 / sqrt(a));  // outside fp32, or not finite
+  double y = rsqrtf(static_cast<float>(a));
+  y = y * (1.5 - 0.5 * a * y * y);
+  y = y * (1.5 - 0.5 * a * y * y);
+  return static_cast<float>(y);
+}
+
+struct NormParams {
+  const void *x, *res, *w;
+  int64_t t;
+  int nvec;  // k / 8
+  double inv_k, eps;
+  int w_f32;
+  void* h;
+  uint4 *xn, *xhat;
+  uint2* xq;
+  float *xscale, *rstd;
+  uint32_t* status;
+};
+
+constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+
+// Sum over the row's threads, the same value in each of them.
+template <int TPR, class T>
+__device__ __forceinline__ T row_sum(T v, T* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v += part[i];
+  }
+  return v;
+}
+
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (TPR > 32) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v = max(v, part[i]);
+  }
+  return v;
+}
+
+template <bool XF32, bool HF32, int TPR, int R>
+__global__ void __launch_bounds__(norm_block(TPR)) k_rmsnorm(const NormParams p) {
+  __shared__ double s_sum[norm_block(TPR) / 32];
+  __shared__ uint32_t s_max[norm_block(TPR) / 32];
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kRows = norm_block(TPR) / TPR;
+  const int tid = threadIdx.x % TPR;
+  const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
+  if (row >= p.t) return;  // whole warps: with more than one row a block, a row is one warp
+  const int64_t base = row * p.nvec;
+
+  float h[R][8];
+  double ss = 0.0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = r * TPR + tid;
+    if (i < p.nvec) {
+      load8<XF32>(p.x, base + i, h[r]);
+      if (p.res != nullptr) {
+        float q[8];
+        load8<HF32>(p.res, base + i, q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[r][e] = __fadd_rn(h[r][e], q[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[r][e] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if constexpr (!HF32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[r][e] = __bfloat162float(__float2bfloat16_rn(h[r][e]));
+    }
+    const int i = r * TPR + tid;
+    if (p.h != nullptr && i < p.nvec) store8<HF32>(p.h, base + i, h[r]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = h[r][e];
+      ss = fma(d, d, ss);
+    }
+  }
+  ss = row_sum<TPR>(ss, s_sum);
+  const float rstd = inverse_root(fma(ss, p.inv_k, p.eps));
+  if (tid == 0) {
+    if (p.rstd != nullptr) p.rstd[row] = rstd;
+    if (!(ss < __longlong_as_double(0x7FF0000000000000ll))) raise_status(p.status, SBL_STATUS_NONFINITE_X);
+  }
+  if (p.xn == nullptr && p.xhat == nullptr && p.xq == nullptr && p.xscale == nullptr) return;
+
+  uint4 v[R];
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = r * TPR + tid;
+    v[r] = make_uint4(0, 0, 0, 0);
+    if (i < p.nvec) {
+      float n[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(h[r][e], rstd);
+      if (p.w != nullptr) {
+        float w[8];
+        if (p.w_f32)
+          load8<true>(p.w, i, w);
+        else
+          load8<false>(p.w, i, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(n[e], w[e]);
+      }
+      v[r] = pack8(n);
+      if (p.xn != nullptr) p.xn[base + i] = v[r];
+    }
+    m2 = __vmaxu2(m2, v[r].x & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, v[r].y & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, v[r].z & 0x7FFF7FFFu);
+    m2 = __vmaxu2(m2, v[r].w & 0x7FFF7FFFu);
+  }
+  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+  if (m >= 0x7F80u) raise_status(p.status, SBL_STATUS_NONFINITE_X);
+  if (p.xhat == nullptr && p.xq == nullptr && p.xscale == nullptr) return;
+
+  m = row_max<TPR>(m, s_max);
+  const float ap = fmaxf(__uint_as_float(m << 16), 1e-5f);
+  if (tid == 0 && p.xscale != nullptr) p.xscale[row] = ap;
+  const QScale qs = make_qscale(ap);
+  const float a_over_127 = __fdiv_rn(ap, 127.0f);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = r * TPR + tid;
+    if (i < p.nvec) {
+      const uint2 c = quantise8(v[r], qs);
+      if (p.xq != nullptr) p.xq[base + i] = c;
+      if (p.xhat != nullptr) p.xhat[base + i] = qs.exact ? dequantise8(v[r], qs) : dequant8_fast(c, a_over_127);
+    }
+  }
+}
+
+template <bool XF32, bool HF32, int TPR, int R>
+cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
+  constexpr int rows = norm_block(TPR) / TPR;
+  return launch_pdl(k_rmsnorm<XF32, HF32, TPR, R>, dim3(static_cast<unsigned>((p.t + rows - 1) / rows)),
+                    dim3(norm_block(TPR)), 0, s, p);
+}
+
+// Threads a row: as few as hold it with four vectors each, for the most rows
+// in flight.
+template <bool XF32, bool HF32>
+cudaError_t pick_norm(const NormParams& p, cudaStream_t s) {
+  const int n = p.nvec;
+  if (n <= 32) return launch_norm<XF32, HF32, 32, 1>(p, s);
+  if (n <= 64) return launch_norm<XF32, HF32, 32, 2>(p, s);
+  if (n <= 96) return launch_norm<XF32, HF32, 32, 3>(p, s);
+  if (n <= 128) return launch_norm<XF32, HF32, 32, 4>(p, s);
+  if (n <= 256) return launch_norm<XF32, HF32, 128, 2>(p, s);
+  if (n <= 384) return launch_norm<XF32, HF32, 128, 3>(p, s);
+  if (n <= 512) return launch_norm<XF32, HF32, 128, 4>(p, s);
+  if (n <= 1024) return launch_norm<XF32, HF32, 512, 2>(p, s);
+  if (n <= 1536) return launch_norm<XF32, HF32, 512, 3>(p, s);
+  return launch_norm<XF32, HF32, 512, 4>(p, s);
+}
+
+// ---------------------------------------------------------------------------
+// Backward: g = sum dy, n = h rstd, c = mean(w g n),
+//   dh = dres + rstd (w g - n c),   dw = sum over rows of g n.
+// A group of threads walks rows with a fixed stride and keeps its columns'
+// share of dw in registers; the groups of a block add theirs in shared memory
+// in a fixed order, one row of partial sums a block goes to the workspace,
+// and a second launch adds those, in a fixed order too.
+// ---------------------------------------------------------------------------
+struct NormBwdParams {
+  const void* h;
+  const float* rstd;
+  const void* w;
+  const void* dy[3];
+  int ndy;
+  const void* dres;
+  int64_t t;
+  int nvec;
+  float inv_k;
+  int w_f32;
+  void* dh;
+  uint4* dx;
+  float* part;  // [gridDim.x][k], or nullptr without dw
+};
+
+constexpr int kNormBwdBlock(int tpr) { return tpr < 128 ? 256 : 512; }
+
+// The row's threads wait for each other (its own barrier for each group).
+template <int TPR>
+__device__ __forceinline__ void group_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+}
+
+template <bool HF32, bool DF32, int TPR, int R>
+__global__ void __launch_bounds__(kNormBwdBlock(TPR), 1) k_rmsnorm_bwd(const NormBwdParams p) {
+  constexpr int kBlock = kNormBwdBlock(TPR), kGroups = kBlock / TPR, kWarps = TPR / 32;
+  __shared__ float s_part[2][kGroups][kWarps];
+  __shared__ float4 s_dw[kGroups > 1 ? TPR * R * 2 : 1];
+  pdl_wait();
+  pdl_trigger();
+  const int group = threadIdx.x / TPR, tid = threadIdx.x % TPR, lane = threadIdx.x & 31, warp = tid >> 5;
+  float acc[R][8];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[r][e] = 0.0f;
+
+  int parity = 0;
+  for (int64_t row = int64_t(blockIdx.x) * kGroups + group; row < p.t; row += int64_t(gridDim.x) * kGroups) {
+    const int64_t base = row * p.nvec;
+    const float rstd = p.rstd[row];
+    float n[R][8], g[R][8];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * TPR + tid;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[r][e] = g[r][e] = 0.0f;
+      if (i < p.nvec) {
+        load8<HF32>(p.h, base + i, n[r]);
+        load8<DF32>(p.dy[0], base + i, g[r]);
+        float q[8];
+        if (p.ndy > 1) {
+          load8<DF32>(p.dy[1], base + i, q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[r][e] += q[e];
+        }
+        if (p.ndy > 2) {
+          load8<DF32>(p.dy[2], base + i, q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[r][e] += q[e];
+        }
+      }
+    }
+    float c = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * TPR + tid;
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+      if (p.w != nullptr && i < p.nvec) {
+        if (p.w_f32)
+          load8<true>(p.w, i, w);
+        else
+          load8<false>(p.w, i, w);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[r][e] *= rstd;
+        acc[r][e] = fmaf(g[r][e], n[r][e], acc[r][e]);
+        g[r][e] *= w[e];
+        c = fmaf(g[r][e], n[r][e], c);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if constexpr (TPR > 32) {
+      if (lane == 0) s_part[parity][group][warp] = c;
+      group_sync<TPR>(group);
+      c = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) c += s_part[parity][group][i];
+      parity ^= 1;  // a slot is written again two rows on, behind another barrier
+    }
+    c *= p.inv_k;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * TPR + tid;
+      if (i >= p.nvec) continue;
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = rstd * fmaf(-n[r][e], c, g[r][e]);
+      if (p.dres != nullptr) {
+        float q[8];
+        load8<HF32>(p.dres, base + i, q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] += q[e];
+      }
+      store8<HF32>(p.dh, base + i, d);
+      if (p.dx != nullptr) p.dx[base + i] = pack8(d);
+    }
+  }
+  if (p.part == nullptr) return;
+  float4* dst = reinterpret_cast<float4*>(p.part) + int64_t(blockIdx.x) * (2 * p.nvec);
+  if constexpr (kGroups == 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * TPR + tid;
+      if (i >= p.nvec) continue;
+      dst[2 * i] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+      dst[2 * i + 1] = make_float4(acc[r][4], acc[r][5], acc[r][6], acc[r][7]);
+    }
+  } else {  // the groups' shares, one group after the other
+    for (int gr = 0; gr < kGroups; ++gr) {
+      if (group == gr) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          float4* s = s_dw + 2 * (r * TPR + tid);
+          float4 a = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
+          float4 b = make_float4(acc[r][4], acc[r][5], acc[r][6], acc[r][7]);
+          if (gr > 0) {
+            a.x += s[0].x, a.y += s[0].y, a.z += s[0].z, a.w += s[0].w;
+            b.x += s[1].x, b.y += s[1].y, b.z += s[1].z, b.w += s[1].w;
+          }
+          s[0] = a, s[1] = b;
+        }
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < 2 * p.nvec; i += kBlock) dst[i] = s_dw[i];
+  }
+}
+
+// dw[c] = sum of the blocks' partial sums: 8 threads of 4 columns across, 32 rows of
+// partial sums at a time, then a tree over the 32.
+__global__ void __launch_bounds__(256) k_norm_dw(const float4* __restrict__ part, int blocks, int n4, float4* dw) {
+  __shared__ float4 s[32][8];
+  pdl_wait();
+  pdl_trigger();
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int col = blockIdx.x * 8 + x;
+  float4 a = make_float4(0, 0, 0, 0);
+  if (col < n4)
+    for (int b = y; b < blocks; b += 32) {
+      const float4 v = __ldcg(part + int64_t(b) * n4 + col);
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
+  s[y][x] = a;
+  for (int o = 16; o > 0; o >>= 1) {
+    __syncthreads();
+    if (y < o) {
+      const float4 v = s[y + o][x];
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+      s[y][x] = a;
+    }
+  }
+  if (y == 0 && col < n4) dw[col] = a;
+}
+
+template <bool HF32, bool DF32, int TPR, int R>
+cudaError_t launch_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t s) {
+  constexpr int block = kNormBwdBlock(TPR), groups = block / TPR;
+  const int64_t want = (p.t + groups - 1) / groups;
+  const int blocks = static_cast<int>(want < num_sms ? want : num_sms);
+  const cudaError_t e =
+      launch_pdl(k_rmsnorm_bwd<HF32, DF32, TPR, R>, dim3(blocks), dim3(block), 0, s, p);
+  if (e != cudaSuccess || dw == nullptr) return e;
+  const int n4 = 2 * p.nvec;
+  return launch_pdl(k_norm_dw, dim3((n4 + 7) / 8), dim3(256), 0, s, reinterpret_cast<const float4*>(p.part), blocks,
+                    n4, reinterpret_cast<float4*>(dw));
+}
+
+template <bool HF32, bool DF32>
+cudaError_t pick_norm_bwd(const NormBwdParams& p, float* dw, int num_sms, cudaStream_t s) {
+  const int n = p.nvec;
+  if (n <= 32) return launch_norm_bwd<HF32, DF32, 32, 1>(p, dw, num_sms, s);
+  if (n <= 64) return launch_norm_bwd<HF32, DF32, 32, 2>(p, dw, num_sms, s);
+  if (n <= 128) return launch_norm_bwd<HF32, DF32, 32, 4>(p, dw, num_sms, s);
+  if (n <= 256) return launch_norm_bwd<HF32, DF32, 128, 2>(p, dw, num_sms, s);
+  if (n <= 384) return launch_norm_bwd<HF32, DF32, 128, 3>(p, dw, num_sms, s);
+  if (n <= 512) return launch_norm_bwd<HF32, DF32, 128, 4>(p, dw, num_sms, s);
+  if (n <= 1024) return launch_norm_bwd<HF32, DF32, 512, 2>(p, dw, num_sms, s);
+  if (n <= 1536) return launch_norm_bwd<HF32, DF32, 512, 3>(p, dw, num_sms, s);
+  return launch_norm_bwd<HF32, DF32, 512, 4>(p, dw, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t s) {
+  NormParams p;
+  p.x = a.x, p.res = a.residual, p.w = a.weight;
+  p.t = a.t, p.nvec = static_cast<int>(a.k / 8);
+  p.inv_k = 1.0 / static_cast<double>(a.k), p.eps = a.eps;
+  p.w_f32 = (a.flags & SBL_NORM_W_F32) != 0u;
+  p.h = a.h;
+  p.xn = static_cast<uint4*>(a.xn), p.xhat = static_cast<uint4*>(a.xhat), p.xq = reinterpret_cast<uint2*>(a.xq);
+  p.xscale = a.xscale, p.rstd = a.rstd, p.status = a.status;
+  const bool xf = (a.flags & SBL_NORM_X_F32) != 0u;
+  const bool hf = a.residual != nullptr ? (a.flags & SBL_NORM_STREAM_F32) != 0u : xf;
+  if (xf) return hf ? pick_norm<true, true>(p, s) : pick_norm<true, false>(p, s);
+  return hf ? pick_norm<false, true>(p, s) : pick_norm<false, false>(p, s);
+}
+
+int64_t rmsnorm_bwd_max_blocks(int64_t t) { return t < kNormBwdMaxBlocks ? t : kNormBwdMaxBlocks; }
+
+cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
+  NormBwdParams p;
+  p.h = a.h, p.rstd = a.rstd, p.w = a.weight;
+  for (int i = 0; i < 3; ++i) p.dy[i] = i < a.dy_count ? a.dys[i] : nullptr;
+  p.ndy = a.dy_count, p.dres = a.dres;
+  p.t = a.t, p.nvec = static_cast<int>(a.k / 8);
+  p.inv_k = 1.0f / static_cast<float>(a.k);
+  p.w_f32 = (a.flags & SBL_NORM_W_F32) != 0u;
+  p.dh = a.dh, p.dx = static_cast<uint4*>(a.dx);
+  p.part = a.dw != nullptr ? static_cast<float*>(a.workspace) : nullptr;
+  if (num_sms > kNormBwdMaxBlocks) num_sms = kNormBwdMaxBlocks;
+  const bool hf = (a.flags & SBL_NORM_STREAM_F32) != 0u, df = (a.flags & SBL_NORM_DY_F32) != 0u;
+  if (hf) return df ? pick_norm_bwd<true, true>(p, a.dw, num_sms, s) : pick_norm_bwd<true, false>(p, a.dw, num_sms, s);
+  return df ? pick_norm_bwd<false, true>(p, a.dw, num_sms, s) : pick_norm_bwd<false, false>(p, a.dw, num_sms, s);
+}
+
+}  // namespace sbl

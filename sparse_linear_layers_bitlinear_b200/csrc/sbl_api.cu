@@ -14,27 +14,21 @@ namespace {
 std::atomic<uint64_t> g_launches{0};
 }  // namespace
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
-}  // namespace sbl
 
 namespace {
-
-constexpr int64_t kMaxK = 131072;  // keeps |acc| <= 127 * k below 2^24: (float)acc is exact
-constexpr uint32_t kLayerFlags = SBL_PACK_GEMV | SBL_MASK_FROM_QUANT | SBL_PACK_GEMV_6BIT | SBL_FUSE_ACT_QUANT;
-constexpr uint32_t kBackwardFlags = SBL_GRAD_F32 | SBL_NO_DX | SBL_NO_DW | SBL_MASKED_GRAD | SBL_DW_QUANT_X;
-
 struct DeviceInfo {
   bool checked = false;
   bool ok = false;
   int num_sms = 0;
 };
 
-DeviceInfo g_devices[64];
+DeviceInfo g_devices[kMaxDevices];
 std::mutex g_dev_mutex;
+}  // namespace
 
-// Current device must be sm_100 (B200).  Cached per device ordinal.
 sbl_status current_device(int* num_sms) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SBL_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SBL_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   DeviceInfo& d = g_devices[dev];
   if (!d.checked) {
@@ -48,6 +42,14 @@ sbl_status current_device(int* num_sms) {
   *num_sms = d.num_sms;
   return SBL_OK;
 }
+
+}  // namespace sbl
+
+namespace {
+
+constexpr int64_t kMaxK = 131072;  // keeps |acc| <= 127 * k below 2^24: (float)acc is exact
+constexpr uint32_t kLayerFlags = SBL_PACK_GEMV | SBL_MASK_FROM_QUANT | SBL_PACK_GEMV_6BIT | SBL_FUSE_ACT_QUANT;
+constexpr uint32_t kBackwardFlags = SBL_GRAD_F32 | SBL_NO_DX | SBL_NO_DW | SBL_MASKED_GRAD | SBL_DW_QUANT_X;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,0 +1,199 @@
+// C ABI of the operators around the products (norm, AdamW, linear cross
+// entropy): argument checks and dispatch.  See include/sbl.h for the contract.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "sbl_kernels.h"
+
+using namespace sbl;
+
+namespace {
+
+constexpr uint32_t kNormFwdFlags = SBL_NORM_X_F32 | SBL_NORM_STREAM_F32 | SBL_NORM_W_F32;
+constexpr uint32_t kNormBwdFlags = SBL_NORM_STREAM_F32 | SBL_NORM_W_F32 | SBL_NORM_DY_F32;
+constexpr uint32_t kAdamFlags = SBL_ADAMW_GRAD_F32 | SBL_ADAMW_STATE_8BIT | SBL_ADAMW_NO_DECAY;
+constexpr int64_t kMaxRows = int64_t(1) << 30;
+constexpr int64_t kCeMaxRows = int64_t(1) << 22, kCeMaxD = 131072;
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool all_aligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned(p, 16)) return false;
+  return true;
+}
+
+sbl_status code(cudaError_t e) { return e == cudaSuccess ? SBL_OK : SBL_ERR_CUDA; }
+
+bool norm_shape(int64_t t, int64_t k) {
+  return t >= 0 && t <= kMaxRows && k >= 8 && k % 8 == 0 && k <= SBL_NORM_MAX_K;
+}
+
+bool ce_shape(int64_t t, int64_t v, int64_t d) {
+  return t >= 0 && t <= kCeMaxRows && v >= 1 && v <= kCeMaxRows && d >= 8 && d % 8 == 0 && d <= kCeMaxD;
+}
+
+bool factor(double x) { return std::isfinite(x) && x >= 0.0; }
+
+}  // namespace
+
+extern "C" {
+
+sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* weight, int64_t t, int64_t k,
+                               double eps, uint32_t flags, void* h_out, void* xn_out, void* xhat_out, int8_t* xq_out,
+                               float* xscale_out, float* rstd_out, uint32_t* status_dev, sbl_stream_t stream) {
+  if ((flags & ~kNormFwdFlags) != 0u) return SBL_ERR_INVALID_ARG;
+  if (!norm_shape(t, k)) return SBL_ERR_SHAPE;
+  if (!(eps >= 1e-12 && eps <= 1.0)) return SBL_ERR_INVALID_ARG;
+  if (t == 0) return SBL_OK;
+  if (x == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!h_out && !xn_out && !xhat_out && !xq_out && !xscale_out && !rstd_out) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({x, residual, weight, h_out, xn_out, xhat_out, xq_out, xscale_out, rstd_out}) ||
+      !aligned(status_dev, 4))
+    return SBL_ERR_ALIGN;
+  int sms = 0;
+  const sbl_status st = current_device(&sms);
+  if (st != SBL_OK) return st;
+  const NormArgs a{x, residual, weight, t, k, eps, flags, h_out, xn_out, xhat_out, xq_out, xscale_out, rstd_out,
+                   status_dev};
+  return code(launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t sbl_rmsnorm_backward_workspace_bytes(int64_t t, int64_t k) {
+  if (!norm_shape(t, k) || t == 0) return 0;
+  return size_t(rmsnorm_bwd_max_blocks(t)) * size_t(k) * 4;
+}
+
+sbl_status sbl_rmsnorm_backward(const void* h, const float* rstd, const void* weight, const void* const* dys,
+                                int32_t dy_count, const void* dres, int64_t t, int64_t k, uint32_t flags, void* dh,
+                                void* dx, float* dw, void* workspace, sbl_stream_t stream) {
+  if ((flags & ~kNormBwdFlags) != 0u || dy_count < 1 || dy_count > 3) return SBL_ERR_INVALID_ARG;
+  if (!norm_shape(t, k)) return SBL_ERR_SHAPE;
+  if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  if (t == 0) {
+    if (dw == nullptr) return SBL_OK;
+    const sbl_status st = current_device(&sms);
+    if (st != SBL_OK) return st;
+    return code(cudaMemsetAsync(dw, 0, size_t(k) * 4, s));
+  }
+  if (h == nullptr || rstd == nullptr || dys == nullptr || dh == nullptr) return SBL_ERR_INVALID_ARG;
+  for (int i = 0; i < dy_count; ++i) {
+    if (dys[i] == nullptr) return SBL_ERR_INVALID_ARG;
+    if (!aligned(dys[i], 16)) return SBL_ERR_ALIGN;
+  }
+  if (dw != nullptr && workspace == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({h, weight, dres, dh, dx, workspace}) || !aligned(rstd, 4)) return SBL_ERR_ALIGN;
+  const sbl_status st = current_device(&sms);
+  if (st != SBL_OK) return st;
+  const NormBwdArgs a{h, rstd, weight, dys, dy_count, dres, t, k, flags, dh, dx, dw, workspace};
+  return code(launch_rmsnorm_bwd(a, sms, s));
+}
+
+sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const sbl_adamw_params* params,
+                          uint32_t* status_dev, sbl_stream_t stream) {
+  if (count < 0 || params == nullptr || (count > 0 && tensors == nullptr)) return SBL_ERR_INVALID_ARG;
+  const sbl_adamw_params& q = *params;
+  if (!(q.beta1 >= 0.0 && q.beta1 < 1.0 && q.beta2 >= 0.0 && q.beta2 < 1.0)) return SBL_ERR_INVALID_ARG;
+  if (!factor(q.lr) || !factor(q.eps) || !factor(q.weight_decay)) return SBL_ERR_INVALID_ARG;
+  if (q.step_dev == nullptr && q.step < 1) return SBL_ERR_INVALID_ARG;
+  if (!aligned(q.lr_dev, 4) || !aligned(q.step_dev, 8) || !aligned(q.grad_scale_dev, 4) || !aligned(status_dev, 4))
+    return SBL_ERR_ALIGN;
+  try {
+    std::vector<const void*> ws;
+    ws.reserve(static_cast<size_t>(count));
+    for (int32_t i = 0; i < count; ++i) {
+      const sbl_adamw_tensor& t = tensors[i];
+      if ((t.flags & ~kAdamFlags) != 0u || t.reserved != 0u) return SBL_ERR_INVALID_ARG;
+      if (t.numel < 0 || t.numel > (int64_t(1) << 40)) return SBL_ERR_SHAPE;
+      if (t.numel == 0) continue;
+      if (t.w == nullptr || t.grad == nullptr || t.m == nullptr || t.v == nullptr) return SBL_ERR_INVALID_ARG;
+      if ((t.flags & SBL_ADAMW_STATE_8BIT) && (t.m_scale == nullptr || t.v_scale == nullptr))
+        return SBL_ERR_INVALID_ARG;
+      if (!all_aligned16({t.w, t.master, t.grad, t.m, t.v}) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+        return SBL_ERR_ALIGN;
+      ws.push_back(t.w);
+    }
+    if (ws.empty()) return SBL_OK;
+    std::sort(ws.begin(), ws.end());
+    if (std::adjacent_find(ws.begin(), ws.end()) != ws.end()) return SBL_ERR_INVALID_ARG;  // the same tensor twice
+    int sms = 0;
+    const sbl_status st = current_device(&sms);
+    if (st != SBL_OK) return st;
+    // up to kAdamMaxTensors a launch, empty ones left out
+    sbl_adamw_tensor batch[kAdamMaxTensors];
+    int n = 0;
+    uint64_t elements = 0;
+    for (int32_t i = 0; i < count; ++i) {
+      if (tensors[i].numel == 0) continue;
+      if (n == kAdamMaxTensors || (n > 0 && elements + uint64_t(tensors[i].numel) > (uint64_t(1) << 41))) {
+        if (launch_adamw(batch, n, q, status_dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+          return SBL_ERR_CUDA;
+        n = 0;
+        elements = 0;
+      }
+      batch[n++] = tensors[i];
+      elements += uint64_t(tensors[i].numel);
+    }
+    return code(launch_adamw(batch, n, q, status_dev, reinterpret_cast<cudaStream_t>(stream)));
+  } catch (const std::bad_alloc&) {
+    return SBL_ERR_INVALID_ARG;  // a count the host cannot hold
+  }
+}
+
+size_t sbl_linear_ce_workspace_bytes(int64_t t, int64_t v, int64_t d, int32_t backward) {
+  if (!ce_shape(t, v, d) || t == 0) return 0;
+  return static_cast<size_t>(linear_ce_workspace(t, v, d, backward != 0));
+}
+
+sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* targets, int64_t t, int64_t v, int64_t d,
+                                 int64_t ignore_index, float* loss, float* lse, void* workspace, uint32_t* status_dev,
+                                 sbl_stream_t stream) {
+  if (!ce_shape(t, v, d)) return SBL_ERR_SHAPE;
+  if (t == 0) return SBL_OK;
+  if (!h || !w || !targets || !loss || !lse || !workspace) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({h, w}) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
+      !aligned(workspace, 256) || !aligned(status_dev, 4))
+    return SBL_ERR_ALIGN;
+  int sms = 0;
+  const sbl_status st = current_device(&sms);
+  if (st != SBL_OK) return st;
+  CeArgs a = {};
+  a.h = static_cast<const uint16_t*>(h), a.w = static_cast<const uint16_t*>(w), a.targets = targets;
+  a.t = t, a.v = v, a.d = d, a.ignore_index = ignore_index;
+  a.loss = loss, a.lse = lse, a.workspace = workspace, a.status = status_dev;
+  return code(launch_linear_ce(a, sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,
+                                  const float* dloss, int64_t dloss_stride, int64_t t, int64_t v, int64_t d,
+                                  int64_t ignore_index, void* dh, void* dw, void* workspace, uint32_t* status_dev,
+                                  sbl_stream_t stream) {
+  if (!ce_shape(t, v, d)) return SBL_ERR_SHAPE;
+  if (dloss_stride != 0 && dloss_stride != 1) return SBL_ERR_INVALID_ARG;
+  if (dw == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int sms = 0;
+  sbl_status st;
+  if (t == 0) {  // no rows: dh is empty and dw = 0
+    if ((st = current_device(&sms)) != SBL_OK) return st;
+    return code(cudaMemsetAsync(dw, 0, size_t(v) * size_t(d) * 2, s));
+  }
+  if (!h || !w || !targets || !lse || !dloss || !dh || !workspace) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({h, w, dh}) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(workspace, 256) ||
+      !aligned(status_dev, 4))
+    return SBL_ERR_ALIGN;
+  if ((st = current_device(&sms)) != SBL_OK) return st;
+  CeArgs a = {};
+  a.h = static_cast<const uint16_t*>(h), a.w = static_cast<const uint16_t*>(w), a.targets = targets;
+  a.t = t, a.v = v, a.d = d, a.ignore_index = ignore_index;
+  a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dloss_stride = dloss_stride;
+  a.dh = static_cast<uint16_t*>(dh), a.dw = static_cast<uint16_t*>(dw);
+  a.workspace = workspace, a.status = status_dev;
+  return code(launch_linear_ce_bwd(a, sms, s));
+}
+
+}  // extern "C"

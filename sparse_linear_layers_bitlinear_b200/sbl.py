@@ -46,6 +46,19 @@ SBL_DW_QUANT_X = 1 << 5
 SBL_STATUS_NONFINITE_W = 1 << 0
 SBL_STATUS_NONFINITE_X = 1 << 1
 SBL_STATUS_TIMEOUT = 1 << 2
+SBL_STATUS_NONFINITE_G = 1 << 3
+SBL_STATUS_BAD_TARGET = 1 << 4
+# norm operand types
+SBL_NORM_X_F32 = 1 << 0
+SBL_NORM_STREAM_F32 = 1 << 1
+SBL_NORM_W_F32 = 1 << 2
+SBL_NORM_DY_F32 = 1 << 3
+SBL_NORM_MAX_K = 16384
+# AdamW tensor flags
+SBL_ADAMW_GRAD_F32 = 1 << 0
+SBL_ADAMW_STATE_8BIT = 1 << 1
+SBL_ADAMW_NO_DECAY = 1 << 2
+SBL_ADAMW_BLOCK = 256
 
 
 class SblError(RuntimeError):
@@ -69,6 +82,17 @@ class sbl_blob_layout(ctypes.Structure):
     _fields_ = [(name, ctypes.c_uint64) for name in (
         "total_bytes", "header", "mask", "codes", "weff_bf16", "sp_values", "sp_meta", "sp_meta_bytes",
         "gemv", "gamma", "g", "status", "scratch", "gemv_bytes")]
+
+
+class sbl_adamw_tensor(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("w", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("numel", ctypes.c_int64), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class sbl_adamw_params(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
+        ("grad_scale_dev", ctypes.c_void_p)]
 
 
 # Every entry point of include/sbl.h with its ctypes signature.
@@ -98,6 +122,13 @@ SIGNATURES = {
     "sbl_weight_abs_sum": (_I32, [_LP, _P, _P, _P]),
     "sbl_prepare_weights_from_sum": (_I32, [_LP, _P, _P, _I64, _P]),
     "sbl_forward_quantized": (_I32, [_LP, _P, _P, _I64, _P, _P, _P]),
+    "sbl_rmsnorm_forward": (_I32, [_P, _P, _P, _I64, _I64, ctypes.c_double, _U32, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sbl_rmsnorm_backward": (_I32, [_P, _P, _P, _P, _I32, _P, _I64, _I64, _U32, _P, _P, _P, _P, _P]),
+    "sbl_rmsnorm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "sbl_adamw_step": (_I32, [_P, _I32, _P, _P, _P]),
+    "sbl_linear_ce_forward": (_I32, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "sbl_linear_ce_backward": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "sbl_linear_ce_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I32]),
 }
 
 _lib = None
@@ -340,6 +371,219 @@ def forward_uses_gemv(layer: Layer, t: int) -> bool:
 def launch_count() -> int:
     """Kernels the library has launched in this process (sbl_launch_count)."""
     return int(lib().sbl_launch_count())
+
+
+# ---------------------------------------------------------------------------
+# The operators around the products: norm, AdamW, linear cross entropy.  They
+# take tensors of several types, so the tensors are checked here (type, length,
+# dense layout, device) before their addresses go to the library.
+# ---------------------------------------------------------------------------
+class _Args:
+    """Checks the tensors of one call and collects their addresses."""
+
+    def __init__(self, what: str):
+        import torch
+
+        self.what = what
+        self.torch = torch
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+    def refuse(self, code: int, why: str):
+        raise SblError(code, f"{self.what}: {why}")
+
+    def __call__(self, t, name: str, dtypes, numel: int, optional: bool = False, at_least: bool = False):
+        """The address of tensor `t`, or None for an optional one that is not there."""
+        if t is None:
+            if not optional:
+                self.refuse(SBL_ERR_INVALID_ARG, f"{name} is missing")
+            return None
+        if t.dtype not in dtypes:
+            self.refuse(SBL_ERR_INVALID_ARG, f"{name} is {t.dtype}, not one of {dtypes}")
+        if not t.is_cuda or t.get_device() != self.device:
+            self.refuse(SBL_ERR_DEVICE, f"{name} is on {t.device}, not on the current CUDA device")
+        if not t.is_contiguous():
+            self.refuse(SBL_ERR_SHAPE, f"{name} is not dense")
+        n = t.numel()
+        if n != numel and not (at_least and n > numel):
+            self.refuse(SBL_ERR_SHAPE, f"{name} has {n} elements, not {numel}")
+        return t.data_ptr()
+
+
+def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h_out=None, xn_out=None, xhat_out=None,
+                    xq_out=None, xscale_out=None, rstd_out=None, status=None, stream=None):
+    """sbl_rmsnorm_forward: h = x + residual, its root-mean-square norm (bf16
+    ``xn_out``) and the norm's int8 codes and scales for ``forward_quantized``
+    (``xq_out``, ``xscale_out``; ``xhat_out``: the values they stand for).
+    x, the stream (residual, h_out) and weight are bf16 or fp32 each; without a
+    residual h_out has x's type.  ``status``: a device int32 tensor or None."""
+    a = _Args("sbl_rmsnorm_forward")
+    T = a.torch
+    bf, f32 = T.bfloat16, T.float32
+    any_, n = (bf, f32), t * k
+    xp = a(x, "x", any_, n)
+    flags = SBL_NORM_X_F32 if x.dtype is f32 else 0
+    stream_type = x.dtype if residual is None else residual.dtype
+    if stream_type is f32:
+        flags |= SBL_NORM_STREAM_F32
+    if weight is not None and weight.dtype is f32:
+        flags |= SBL_NORM_W_F32
+    code = lib().sbl_rmsnorm_forward(
+        xp, a(residual, "residual", any_, n, True), a(weight, "weight", any_, k, True), t, k, eps, flags,
+        a(h_out, "h_out", (stream_type,), n, True), a(xn_out, "xn_out", (bf,), n, True),
+        a(xhat_out, "xhat_out", (bf,), n, True), a(xq_out, "xq_out", (T.int8,), n, True),
+        a(xscale_out, "xscale_out", (f32,), t, True), a(rstd_out, "rstd_out", (f32,), t, True),
+        a(status, "status", (T.int32,), 1, True), _stream(stream))
+    _check(code, "sbl_rmsnorm_forward")
+
+
+def rmsnorm_backward_workspace_bytes(t: int, k: int) -> int:
+    return int(lib().sbl_rmsnorm_backward_workspace_bytes(t, k))
+
+
+def rmsnorm_backward(h, rstd, dys, t: int, k: int, dh, weight=None, dres=None, dx=None, dw=None, workspace=None,
+                     stream=None):
+    """sbl_rmsnorm_backward: the gradient dh of h (and so of x and of the
+    residual) from ``dys`` (one to three gradients of the normalised rows, which
+    are added) and ``dres`` (the residual stream's own gradient or None); dx: a
+    bf16 copy of dh or None; dw: fp32 gradient of the weight or None (it needs
+    ``workspace``, a uint8 tensor of rmsnorm_backward_workspace_bytes)."""
+    a = _Args("sbl_rmsnorm_backward")
+    T = a.torch
+    bf, f32 = T.bfloat16, T.float32
+    any_, n = (bf, f32), t * k
+    if not 1 <= len(dys) <= 3:
+        a.refuse(SBL_ERR_INVALID_ARG, f"{len(dys)} gradients, not 1 to 3")
+    hp = a(h, "h", any_, n)
+    flags = SBL_NORM_STREAM_F32 if h.dtype is f32 else 0
+    if weight is not None and weight.dtype is f32:
+        flags |= SBL_NORM_W_F32
+    if dys[0] is not None and dys[0].dtype is f32:
+        flags |= SBL_NORM_DY_F32
+    dyp = (_P * 3)(*[a(d, "dys", (f32 if flags & SBL_NORM_DY_F32 else bf,), n) for d in dys])
+    ws = a(workspace, "workspace", (T.uint8,), rmsnorm_backward_workspace_bytes(t, k), True, True) if dw is not None \
+        else None
+    code = lib().sbl_rmsnorm_backward(
+        hp, a(rstd, "rstd", (f32,), t), a(weight, "weight", any_, k, True), dyp, len(dys),
+        a(dres, "dres", (h.dtype,), n, True), t, k, flags, a(dh, "dh", (h.dtype,), n), a(dx, "dx", (bf,), n, True),
+        a(dw, "dw", (f32,), k, True), ws, _stream(stream))
+    _check(code, "sbl_rmsnorm_backward")
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamW step: bf16 weights ``w``, bf16 or fp32 ``grad``,
+    states ``m`` and ``v`` (fp32, or float8_e4m3fn / uint8 with the fp32 scales
+    ``m_scale`` and ``v_scale``, one per 256 elements), optional fp32 ``master``."""
+
+    w: "object"
+    grad: "object"
+    m: "object"
+    v: "object"
+    m_scale: "object" = None
+    v_scale: "object" = None
+    master: "object" = None
+    decay: bool = True
+
+    @classmethod
+    def allocate(cls, w, grad, bits: int = 32, master: bool = True, decay: bool = True):
+        """Zeroed states for ``w`` (and an fp32 copy of it with ``master``)."""
+        import torch
+
+        n = w.numel()
+        if bits not in (8, 32):
+            raise SblError(SBL_ERR_INVALID_ARG, f"sbl.AdamWTensor: states of {bits} bits, not 8 or 32")
+        dt = torch.float32 if bits == 32 else torch.float8_e4m3fn
+        blocks = (n + SBL_ADAMW_BLOCK - 1) // SBL_ADAMW_BLOCK
+        m, v = (torch.zeros(n, dtype=dt, device=w.device) for _ in range(2))
+        ms, vs = (torch.zeros(blocks, dtype=torch.float32, device=w.device) if bits == 8 else None for _ in range(2))
+        return cls(w, grad, m, v, ms, vs, w.detach().float().reshape(-1) if master else None, decay)
+
+
+class AdamWTensors:
+    """The tensors of ``adamw_step``, checked once; keeps them alive.  Their
+    addresses stay fixed: build a new one when a tensor is reallocated."""
+
+    def __init__(self, tensors):
+        a = _Args("sbl.AdamWTensors")
+        T = a.torch
+        bf, f32 = T.bfloat16, T.float32
+        self.tensors = list(tensors)
+        self.count = len(self.tensors)
+        self.device = a.device
+        self.array = (sbl_adamw_tensor * max(self.count, 1))()
+        for c, p in zip(self.array, self.tensors):
+            if p.w is None or p.grad is None or p.m is None:
+                a.refuse(SBL_ERR_INVALID_ARG, "w, grad or m is missing")
+            n = p.w.numel()
+            c.numel = n
+            eight = p.m.dtype is not f32
+            c.flags = ((SBL_ADAMW_GRAD_F32 if p.grad.dtype is f32 else 0) | (SBL_ADAMW_STATE_8BIT if eight else 0)
+                       | (0 if p.decay else SBL_ADAMW_NO_DECAY))
+            c.w = a(p.w, "w", (bf,), n)
+            c.grad = a(p.grad, "grad", (bf, f32), n)
+            state = (T.float8_e4m3fn, T.uint8) if eight else (f32,)
+            c.m = a(p.m, "m", state, n)
+            c.v = a(p.v, "v", state, n)
+            c.master = a(p.master, "master", (f32,), n, True)
+            if eight:
+                blocks = (n + SBL_ADAMW_BLOCK - 1) // SBL_ADAMW_BLOCK
+                c.m_scale = a(p.m_scale, "m_scale", (f32,), blocks)
+                c.v_scale = a(p.v_scale, "v_scale", (f32,), blocks)
+
+
+def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95,
+               eps: float = 1e-8, weight_decay: float = 0.0, lr_dev=None, step_dev=None, grad_scale_dev=None,
+               status=None, stream=None):
+    """sbl_adamw_step: one step (the first is ``step`` 1) on every tensor.
+    ``lr_dev`` (fp32), ``step_dev`` (int64) and ``grad_scale_dev`` (fp32) are
+    device scalars that a captured graph reads at each replay, or None."""
+    a = _Args("sbl_adamw_step")
+    T = a.torch
+    if tensors.device != a.device:
+        a.refuse(SBL_ERR_DEVICE, "the tensors are not on the current CUDA device")
+    params = sbl_adamw_params(lr, beta1, beta2, eps, weight_decay, step,
+                              a(lr_dev, "lr_dev", (T.float32,), 1, True), a(step_dev, "step_dev", (T.int64,), 1, True),
+                              a(grad_scale_dev, "grad_scale_dev", (T.float32,), 1, True))
+    _check(lib().sbl_adamw_step(tensors.array, tensors.count, ctypes.byref(params),
+                                a(status, "status", (T.int32,), 1, True), _stream(stream)), "sbl_adamw_step")
+
+
+def linear_ce_workspace_bytes(t: int, v: int, d: int, backward: bool = False) -> int:
+    return int(lib().sbl_linear_ce_workspace_bytes(t, v, d, 1 if backward else 0))
+
+
+def linear_ce_forward(h, w, targets, t: int, v: int, d: int, loss, lse, workspace, ignore_index: int = -100,
+                      status=None, stream=None):
+    """sbl_linear_ce_forward: loss[i] = log sum exp(h[i] w^T) - (h[i] w^T)[targets[i]]
+    and lse, the logits never in memory.  h: bf16 [t, d], w: bf16 [v, d],
+    targets: int64 [t], workspace: uint8, linear_ce_workspace_bytes(t, v, d)."""
+    a = _Args("sbl_linear_ce_forward")
+    T = a.torch
+    bf, f32 = (T.bfloat16,), (T.float32,)
+    code = lib().sbl_linear_ce_forward(
+        a(h, "h", bf, t * d), a(w, "w", bf, v * d), a(targets, "targets", (T.int64,), t), t, v, d, ignore_index,
+        a(loss, "loss", f32, t), a(lse, "lse", f32, t),
+        a(workspace, "workspace", (T.uint8,), linear_ce_workspace_bytes(t, v, d), False, True),
+        a(status, "status", (T.int32,), 1, True), _stream(stream))
+    _check(code, "sbl_linear_ce_forward")
+
+
+def linear_ce_backward(h, w, targets, lse, dloss, t: int, v: int, d: int, dh, dw, workspace,
+                       ignore_index: int = -100, status=None, stream=None):
+    """sbl_linear_ce_backward: dh (bf16 [t, d]) and dw (bf16 [v, d]) from the
+    forward's lse and ``dloss``, fp32 of t elements (each loss's gradient) or of
+    one (the same for all).  workspace: linear_ce_workspace_bytes(t, v, d, True)."""
+    a = _Args("sbl_linear_ce_backward")
+    T = a.torch
+    bf, f32 = (T.bfloat16,), (T.float32,)
+    one = dloss is not None and dloss.numel() == 1
+    code = lib().sbl_linear_ce_backward(
+        a(h, "h", bf, t * d), a(w, "w", bf, v * d), a(targets, "targets", (T.int64,), t), a(lse, "lse", f32, t),
+        a(dloss, "dloss", f32, 1 if one else t), 0 if one else 1, t, v, d, ignore_index, a(dh, "dh", bf, t * d),
+        a(dw, "dw", bf, v * d),
+        a(workspace, "workspace", (T.uint8,), linear_ce_workspace_bytes(t, v, d, True), False, True),
+        a(status, "status", (T.int32,), 1, True), _stream(stream))
+    _check(code, "sbl_linear_ce_backward")
 
 
 class SparseBitLinear:
