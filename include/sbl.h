@@ -425,7 +425,8 @@ typedef struct sbl_adamw_params {
   const float* grad_scale_dev; /* and the factor on every gradient (clipping, loss scale); NULL: 1 */
 } sbl_adamw_params;
 
-/* One AdamW step on `count` tensors (any number; up to 128 go in one launch):
+/* One AdamW step on `count` tensors (any number; up to 128 with the same kind of
+ * states go in one launch):
  *   g = grad grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   value -= lr weight_decay value;  value -= lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
  *   w = RN_bf16(value), value in `master` (or in w)

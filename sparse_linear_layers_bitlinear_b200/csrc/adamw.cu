@@ -28,7 +28,9 @@ namespace sbl {
 namespace {
 
 constexpr int kAdamThreads = 256;
-constexpr int kAdamChunk = 4096;  // elements of one tensor that a block updates
+// Elements of one tensor that a block updates: 16 a thread with fp32 states,
+// one 8-bit block a warp.
+constexpr int chunk_of(bool eight) { return eight ? kAdamThreads / 32 * SBL_ADAMW_BLOCK : 16 * kAdamThreads; }
 constexpr float kFlush = 0x1p-100f;
 constexpr float kFp8Max = 448.0f, kFp8Min = 0x1p-9f;
 
@@ -42,54 +44,58 @@ struct AdamEntry {
   uint32_t flags;
 };
 
+// The step's scalars.
+struct AdamStep {
+  float b1, one_b1, b2, one_b2, eps;
+  float keep;      // 1 - lr decay
+  float rate;      // lr / (1 - b1^step)
+  float inv_root;  // 1 / sqrt(1 - b2^step)
+  float scale;     // of the gradients
+};
+
 struct AdamLaunch {
   AdamEntry entry[kAdamMaxTensors];
   uint32_t first[kAdamMaxTensors + 1];  // first chunk of each tensor
   int count;
-  float lr, b1, one_b1, b2, one_b2, eps, decay;
-  float c1, c2;          // 1 - beta^step
-  double log_b1, log_b2; // for step_dev
+  AdamStep step;
+  // for the scalars that live on the device
+  float lr, decay;
+  double log_b1, log_b2, n;
   const float* lr_dev;
   const int64_t* step_dev;
   const float* grad_scale_dev;
   uint32_t* status;
 };
 
-// The step's scalars.
-struct AdamStep {
-  float b1, one_b1, b2, one_b2, eps;
-  float keep;      // 1 - lr decay
-  float rate;      // lr / c1
-  float inv_root;  // 1 / sqrt(c2)
-  float scale;     // of the gradients
-};
-
 __device__ __forceinline__ AdamStep adam_step(const AdamLaunch& p, bool no_decay) {
-  AdamStep s;
-  s.b1 = p.b1, s.one_b1 = p.one_b1, s.b2 = p.b2, s.one_b2 = p.one_b2, s.eps = p.eps;
-  const float lr = p.lr_dev != nullptr ? *p.lr_dev : p.lr;
-  float c1 = p.c1, c2 = p.c2;
-  if (p.step_dev != nullptr) {
-    const double n = static_cast<double>(*p.step_dev);
-    c1 = static_cast<float>(-expm1(n * p.log_b1));
-    c2 = static_cast<float>(-expm1(n * p.log_b2));
+  AdamStep s = p.step;
+  if (p.lr_dev != nullptr || p.step_dev != nullptr) {
+    const float lr = p.lr_dev != nullptr ? *p.lr_dev : p.lr;
+    const double n = p.step_dev != nullptr ? static_cast<double>(*p.step_dev) : p.n;
+    s.keep = 1.0f - lr * p.decay;
+    s.rate = lr / static_cast<float>(-expm1(n * p.log_b1));
+    s.inv_root = 1.0f / sqrtf(static_cast<float>(-expm1(n * p.log_b2)));
   }
-  s.keep = no_decay ? 1.0f : 1.0f - lr * p.decay;
-  s.rate = lr / c1;
-  s.inv_root = 1.0f / sqrtf(c2);
-  s.scale = p.grad_scale_dev != nullptr ? *p.grad_scale_dev : 1.0f;
+  if (no_decay) s.keep = 1.0f;
+  if (p.grad_scale_dev != nullptr) s.scale = *p.grad_scale_dev;
   return s;
 }
 
-// One element; m, v and value are updated.
-__device__ __forceinline__ void adam_element(const AdamStep& s, float grad, float& m, float& v, float& value,
-                                             bool& bad) {
-  const float g = grad * s.scale;
-  bad |= !(fabsf(g) <= 3.402823466e38f);
-  m = fmaf(s.b1, m, s.one_b1 * g);
-  v = fmaf(s.b2, v, s.one_b2 * g * g);
-  const float den = fmaf(sqrtf(v), s.inv_root, s.eps);
-  value = fmaf(value, s.keep, -(s.rate * m) / den);
+// One element; m, v and value are updated.  Returns sqrt(v).  The moments'
+// products and sums are rounded one by one (no fused multiply-add) and the root
+// is the IEEE one: behind them stands the rounding to 8 bits, where one unit in
+// the last place decides between two codes 6 to 12 % apart.  With the roundings
+// pinned, the states are the same on every build and in any plain form.
+__device__ __forceinline__ float adam_element(const AdamStep& s, float grad, float& m, float& v, float& value,
+                                              uint32_t& bad) {
+  const float g = __fmul_rn(grad, s.scale);
+  bad = max(bad, __float_as_uint(g) & 0x7FFFFFFFu);
+  m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.one_b1, g));
+  v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(__fmul_rn(s.one_b2, g), g));
+  const float root = __fsqrt_rn(v);
+  // the quotient is off by two units at most; nothing rounds behind it
+  value = fmaf(value, s.keep, -__fdividef(s.rate * m, fmaf(root, s.inv_root, s.eps)));
+  return root;
 }
 
 template <bool F32>
@@ -136,12 +142,12 @@ __device__ __forceinline__ uint32_t to_fp8(const float (&f)[4]) {
 }
 
 template <bool GF32, bool MASTER>
-__device__ __forceinline__ void update_fp32(const AdamEntry& t, const AdamStep& s, int64_t first, bool& bad) {
-  constexpr int U = kAdamChunk / (4 * kAdamThreads);
+__device__ __forceinline__ void update_fp32(const AdamEntry& t, const AdamStep& s, int64_t first, uint32_t& bad) {
+  constexpr int kChunk = chunk_of(false), U = kChunk / (4 * kAdamThreads);
   float* mp = static_cast<float*>(t.m);
   float* vp = static_cast<float*>(t.v);
   const int64_t at = first + 4 * threadIdx.x;
-  if (first + kAdamChunk <= t.numel) {
+  if (first + kChunk <= t.numel) {
     float g[U][4], m[U][4], v[U][4], x[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -178,94 +184,100 @@ __device__ __forceinline__ float warp_top(float top) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
-// A block of 256 elements by one warp: lane l holds elements 4 l .. 4 l + 3
-// and 128 more on.
+// A block of 256 elements by one warp, 8 consecutive ones a lane.
 template <bool GF32, bool MASTER>
-__device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s, int64_t first, bool& bad) {
+__device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s, int64_t first, uint32_t& bad) {
   const int lane = threadIdx.x & 31;
+  const int64_t start = first + (threadIdx.x >> 5) * SBL_ADAMW_BLOCK;
+  if (start >= t.numel) return;
+  const int64_t block = start / SBL_ADAMW_BLOCK;
   uint8_t* mp = static_cast<uint8_t*>(t.m);
   uint8_t* vp = static_cast<uint8_t*>(t.v);
-  for (int b = threadIdx.x >> 5; b < kAdamChunk / SBL_ADAMW_BLOCK; b += kAdamThreads / 32) {
-    const int64_t start = first + b * SBL_ADAMW_BLOCK;
-    if (start >= t.numel) return;
-    const int64_t block = start / SBL_ADAMW_BLOCK;
-    const float ms = t.m_scale[block], vs = t.v_scale[block];
-    float g[2][4], m[2][4], v[2][4], x[2][4];
-    const bool full = start + SBL_ADAMW_BLOCK <= t.numel;
+  const int64_t i = start + 8 * lane;
+  const bool full = start + SBL_ADAMW_BLOCK <= t.numel;
+  float g[2][4], m[2][4], v[2][4], x[2][4];
+  uint2 mw = make_uint2(0, 0), vw = make_uint2(0, 0);
+  const float ms = t.m_scale[block], vs = t.v_scale[block];
+  if (full) {
+    mw = *reinterpret_cast<const uint2*>(mp + i);
+    vw = *reinterpret_cast<const uint2*>(vp + i);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t i = start + 128 * h + 4 * lane;
-      if (full) {
-        load4<GF32>(t.grad, i, g[h]);
-        load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i, x[h]);
-        from_fp8(*reinterpret_cast<const uint32_t*>(mp + i), m[h]);
-        from_fp8(*reinterpret_cast<const uint32_t*>(vp + i), v[h]);
-      } else {
-        uint32_t mw = 0, vw = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool in = i + e < t.numel;
-          g[h][e] = in ? load1(t.grad, i + e, GF32) : 0.0f;
-          x[h][e] = in ? (MASTER ? t.master[i + e] : load1(t.w, i + e, false)) : 0.0f;
-          if (in) {
-            mw |= uint32_t(mp[i + e]) << (8 * e);
-            vw |= uint32_t(vp[i + e]) << (8 * e);
-          }
-        }
-        from_fp8(mw, m[h]);
-        from_fp8(vw, v[h]);
-      }
+      load4<GF32>(t.grad, i + 4 * h, g[h]);
+      load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i + 4 * h, x[h]);
     }
-    float mtop = 0.0f, vtop = 0.0f;
+  } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        m[h][e] *= ms;
-        v[h][e] *= vs;
-        v[h][e] *= v[h][e];
-        adam_element(s, g[h][e], m[h][e], v[h][e], x[h][e], bad);
-        v[h][e] = sqrtf(v[h][e]);
-        mtop = fmaxf(mtop, fabsf(m[h][e]));
-        vtop = fmaxf(vtop, v[h][e]);
+        const int64_t j = i + 4 * h + e;
+        const bool in = j < t.numel;
+        g[h][e] = in ? load1(t.grad, j, GF32) : 0.0f;
+        x[h][e] = in ? (MASTER ? t.master[j] : load1(t.w, j, false)) : 0.0f;
+        (h ? mw.y : mw.x) |= in ? uint32_t(mp[j]) << (8 * e) : 0u;
+        (h ? vw.y : vw.x) |= in ? uint32_t(vp[j]) << (8 * e) : 0u;
       }
-    mtop = warp_top(mtop);
-    vtop = warp_top(vtop);
-    const float mi = mtop >= kFlush ? kFp8Max / mtop : 0.0f, vi = vtop >= kFlush ? kFp8Max / vtop : 0.0f;
-    if (lane == 0) {
-      t.m_scale[block] = mtop >= kFlush ? mtop / kFp8Max : 0.0f;
-      t.v_scale[block] = vtop >= kFlush ? vtop / kFp8Max : 0.0f;
+  }
+  from_fp8(mw.x, m[0]);
+  from_fp8(mw.y, m[1]);
+  from_fp8(vw.x, v[0]);
+  from_fp8(vw.y, v[1]);
+  float mtop = 0.0f, vtop = 0.0f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[h][e] = __fmul_rn(m[h][e], ms);
+      v[h][e] = __fmul_rn(v[h][e], vs);
+      v[h][e] = __fmul_rn(v[h][e], v[h][e]);
+      v[h][e] = adam_element(s, g[h][e], m[h][e], v[h][e], x[h][e], bad);
+      mtop = fmaxf(mtop, fabsf(m[h][e]));
+      vtop = fmaxf(vtop, v[h][e]);
     }
+  mtop = warp_top(mtop);
+  vtop = warp_top(vtop);
+  const float mi = mtop >= kFlush ? __fdiv_rn(kFp8Max, mtop) : 0.0f;
+  const float vi = vtop >= kFlush ? __fdiv_rn(kFp8Max, vtop) : 0.0f;
+  if (lane == 0) {
+    t.m_scale[block] = mtop >= kFlush ? __fdiv_rn(mtop, kFp8Max) : 0.0f;
+    t.v_scale[block] = vtop >= kFlush ? __fdiv_rn(vtop, kFp8Max) : 0.0f;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      m[h][e] = __fmul_rn(m[h][e], mi);
+      v[h][e] = __fmul_rn(v[h][e], vi);
+      if (v[h][e] > 0.0f) v[h][e] = fmaxf(v[h][e], kFp8Min);
+    }
+  mw = make_uint2(to_fp8(m[0]), to_fp8(m[1]));
+  vw = make_uint2(to_fp8(v[0]), to_fp8(v[1]));
+  if (full) {
+    *reinterpret_cast<uint2*>(mp + i) = mw;
+    *reinterpret_cast<uint2*>(vp + i) = vw;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t i = start + 128 * h + 4 * lane;
+      if (MASTER) store4(t.master, i + 4 * h, x[h]);
+      store4_bf16(t.w, i + 4 * h, x[h]);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        m[h][e] *= mi;
-        v[h][e] *= vi;
-        if (v[h][e] > 0.0f) v[h][e] = fmaxf(v[h][e], kFp8Min);
+        const int64_t j = i + 4 * h + e;
+        if (j >= t.numel) continue;
+        mp[j] = static_cast<uint8_t>((h ? mw.y : mw.x) >> (8 * e));
+        vp[j] = static_cast<uint8_t>((h ? vw.y : vw.x) >> (8 * e));
+        if (MASTER) t.master[j] = x[h][e];
+        static_cast<__nv_bfloat16*>(t.w)[j] = __float2bfloat16_rn(x[h][e]);
       }
-      const uint32_t mw = to_fp8(m[h]), vw = to_fp8(v[h]);
-      if (full) {
-        *reinterpret_cast<uint32_t*>(mp + i) = mw;
-        *reinterpret_cast<uint32_t*>(vp + i) = vw;
-        if (MASTER) store4(t.master, i, x[h]);
-        store4_bf16(t.w, i, x[h]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (i + e >= t.numel) break;
-          mp[i + e] = static_cast<uint8_t>(mw >> (8 * e));
-          vp[i + e] = static_cast<uint8_t>(vw >> (8 * e));
-          if (MASTER) t.master[i + e] = x[h][e];
-          static_cast<__nv_bfloat16*>(t.w)[i + e] = __float2bfloat16_rn(x[h][e]);
-        }
-      }
-    }
   }
 }
 
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ AdamLaunch p) {
+template <bool EIGHT>
+__global__ void __launch_bounds__(kAdamThreads, EIGHT ? 4 : 2) k_adamw(const __grid_constant__ AdamLaunch p) {
   int lo = 0, hi = p.count - 1;  // the last tensor whose first chunk is not past this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -275,13 +287,13 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
       hi = mid - 1;
   }
   const AdamEntry t = p.entry[lo];
-  const int64_t first = int64_t(blockIdx.x - p.first[lo]) * kAdamChunk;
+  const int64_t first = int64_t(blockIdx.x - p.first[lo]) * chunk_of(EIGHT);
   pdl_wait();
   pdl_trigger();
   const AdamStep s = adam_step(p, (t.flags & SBL_ADAMW_NO_DECAY) != 0u);
-  bool bad = false;
+  uint32_t bad = 0;
   const bool gf = (t.flags & SBL_ADAMW_GRAD_F32) != 0u, master = t.master != nullptr;
-  if (t.flags & SBL_ADAMW_STATE_8BIT) {
+  if constexpr (EIGHT) {
     if (gf)
       master ? update_fp8<true, true>(t, s, first, bad) : update_fp8<true, false>(t, s, first, bad);
     else
@@ -292,35 +304,41 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(const __grid_constant__ 
     else
       master ? update_fp32<false, true>(t, s, first, bad) : update_fp32<false, false>(t, s, first, bad);
   }
-  if (bad) raise_status(p.status, SBL_STATUS_NONFINITE_G);
+  if (bad >= 0x7F800000u) raise_status(p.status, SBL_STATUS_NONFINITE_G);
 }
 
 }  // namespace
 
+// The tensors of a launch all hold their states alike (the first one's way).
 cudaError_t launch_adamw(const sbl_adamw_tensor* tensors, int count, const sbl_adamw_params& q, uint32_t* status,
                          cudaStream_t s) {
   if (count < 1 || count > kAdamMaxTensors) return cudaErrorInvalidValue;
+  const bool eight = (tensors[0].flags & SBL_ADAMW_STATE_8BIT) != 0u;
+  const uint64_t chunk = static_cast<uint64_t>(chunk_of(eight));
   AdamLaunch p = {};
   uint64_t chunks = 0;
   for (int i = 0; i < count; ++i) {
     const sbl_adamw_tensor& t = tensors[i];
     p.entry[i] = AdamEntry{t.w, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.numel, t.flags};
     p.first[i] = static_cast<uint32_t>(chunks);
-    chunks += (uint64_t(t.numel) + kAdamChunk - 1) / kAdamChunk;
+    chunks += (uint64_t(t.numel) + chunk - 1) / chunk;
     if (chunks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   }
   p.first[count] = static_cast<uint32_t>(chunks);
   p.count = count;
-  p.lr = static_cast<float>(q.lr);
-  p.b1 = static_cast<float>(q.beta1), p.one_b1 = static_cast<float>(1.0 - q.beta1);
-  p.b2 = static_cast<float>(q.beta2), p.one_b2 = static_cast<float>(1.0 - q.beta2);
-  p.eps = static_cast<float>(q.eps), p.decay = static_cast<float>(q.weight_decay);
-  p.log_b1 = std::log(q.beta1), p.log_b2 = std::log(q.beta2);
-  p.c1 = static_cast<float>(1.0 - std::pow(q.beta1, double(q.step)));
-  p.c2 = static_cast<float>(1.0 - std::pow(q.beta2, double(q.step)));
+  p.lr = static_cast<float>(q.lr), p.decay = static_cast<float>(q.weight_decay);
+  p.n = static_cast<double>(q.step), p.log_b1 = std::log(q.beta1), p.log_b2 = std::log(q.beta2);
+  p.step.b1 = static_cast<float>(q.beta1), p.step.one_b1 = static_cast<float>(1.0 - q.beta1);
+  p.step.b2 = static_cast<float>(q.beta2), p.step.one_b2 = static_cast<float>(1.0 - q.beta2);
+  p.step.eps = static_cast<float>(q.eps);
+  p.step.keep = static_cast<float>(1.0 - q.lr * q.weight_decay);
+  p.step.rate = static_cast<float>(q.lr / -std::expm1(p.n * p.log_b1));
+  p.step.inv_root = static_cast<float>(1.0 / std::sqrt(-std::expm1(p.n * p.log_b2)));
+  p.step.scale = 1.0f;
   p.lr_dev = q.lr_dev, p.step_dev = q.step_dev, p.grad_scale_dev = q.grad_scale_dev;
   p.status = status;
-  return launch_pdl(k_adamw, dim3(static_cast<unsigned>(chunks)), dim3(kAdamThreads), 0, s, p);
+  return launch_pdl(eight ? k_adamw<true> : k_adamw<false>, dim3(static_cast<unsigned>(chunks)), dim3(kAdamThreads), 0,
+                    s, p);
 }
 
 }  // namespace sbl

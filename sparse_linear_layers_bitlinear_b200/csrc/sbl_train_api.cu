@@ -122,22 +122,29 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
     int sms = 0;
     const sbl_status st = current_device(&sms);
     if (st != SBL_OK) return st;
-    // up to kAdamMaxTensors a launch, empty ones left out
-    sbl_adamw_tensor batch[kAdamMaxTensors];
-    int n = 0;
-    uint64_t elements = 0;
-    for (int32_t i = 0; i < count; ++i) {
-      if (tensors[i].numel == 0) continue;
-      if (n == kAdamMaxTensors || (n > 0 && elements + uint64_t(tensors[i].numel) > (uint64_t(1) << 41))) {
-        if (launch_adamw(batch, n, q, status_dev, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-          return SBL_ERR_CUDA;
+    // up to kAdamMaxTensors of one kind of states a launch, empty ones left out
+    for (const uint32_t kind : {0u, uint32_t(SBL_ADAMW_STATE_8BIT)}) {
+      sbl_adamw_tensor batch[kAdamMaxTensors];
+      int n = 0;
+      uint64_t elements = 0;
+      auto launch = [&] {
+        const int count = n;
         n = 0;
         elements = 0;
+        return count == 0 || launch_adamw(batch, count, q, status_dev, reinterpret_cast<cudaStream_t>(stream)) ==
+                                 cudaSuccess;
+      };
+      for (int32_t i = 0; i < count; ++i) {
+        const sbl_adamw_tensor& t = tensors[i];
+        if (t.numel == 0 || (t.flags & SBL_ADAMW_STATE_8BIT) != kind) continue;
+        if ((n == kAdamMaxTensors || elements + uint64_t(t.numel) > (uint64_t(1) << 41)) && !launch())
+          return SBL_ERR_CUDA;
+        batch[n++] = t;
+        elements += uint64_t(t.numel);
       }
-      batch[n++] = tensors[i];
-      elements += uint64_t(tensors[i].numel);
+      if (!launch()) return SBL_ERR_CUDA;
     }
-    return code(launch_adamw(batch, n, q, status_dev, reinterpret_cast<cudaStream_t>(stream)));
+    return SBL_OK;
   } catch (const std::bad_alloc&) {
     return SBL_ERR_INVALID_ARG;  // a count the host cannot hold
   }

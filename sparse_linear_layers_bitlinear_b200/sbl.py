@@ -378,35 +378,63 @@ def launch_count() -> int:
 # take tensors of several types, so the tensors are checked here (type, length,
 # dense layout, device) before their addresses go to the library.
 # ---------------------------------------------------------------------------
-class _Args:
-    """Checks the tensors of one call and collects their addresses."""
+_types = None  # torch's types, once torch is imported
 
-    def __init__(self, what: str):
+
+class _Types:
+    def __init__(self):
         import torch
 
-        self.what = what
-        self.torch = torch
-        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        self.bf16, self.f32 = (torch.bfloat16,), (torch.float32,)
+        self.float = (torch.bfloat16, torch.float32)
+        self.i8, self.u8, self.i32, self.i64 = (torch.int8,), (torch.uint8,), (torch.int32,), (torch.int64,)
+        self.code8 = (torch.float8_e4m3fn, torch.uint8)
+        self.current_device = torch.cuda.current_device
+        # the raw handle of torch's current stream: a call's cost on the host is most of a small call's time
+        self.raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 
-    def refuse(self, code: int, why: str):
-        raise SblError(code, f"{self.what}: {why}")
 
-    def __call__(self, t, name: str, dtypes, numel: int, optional: bool = False, at_least: bool = False):
-        """The address of tensor `t`, or None for an optional one that is not there."""
-        if t is None:
-            if not optional:
-                self.refuse(SBL_ERR_INVALID_ARG, f"{name} is missing")
-            return None
-        if t.dtype not in dtypes:
-            self.refuse(SBL_ERR_INVALID_ARG, f"{name} is {t.dtype}, not one of {dtypes}")
-        if not t.is_cuda or t.get_device() != self.device:
-            self.refuse(SBL_ERR_DEVICE, f"{name} is on {t.device}, not on the current CUDA device")
-        if not t.is_contiguous():
-            self.refuse(SBL_ERR_SHAPE, f"{name} is not dense")
-        n = t.numel()
-        if n != numel and not (at_least and n > numel):
-            self.refuse(SBL_ERR_SHAPE, f"{name} has {n} elements, not {numel}")
-        return t.data_ptr()
+def _torch_types() -> _Types:
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
+
+
+def _device(T: _Types, what: str, name: str, t) -> int:
+    """The device of a call: that of its first tensor, which has to be the current one."""
+    if t is None:
+        raise SblError(SBL_ERR_INVALID_ARG, f"{what}: {name} is missing")
+    dev = t.get_device()
+    if dev < 0 or dev != T.current_device():
+        raise SblError(SBL_ERR_DEVICE, f"{what}: {name} is on {t.device}, not on the current CUDA device")
+    return dev
+
+
+def _addr(what: str, name: str, t, dtypes, numel: int, dev: int):
+    """The address of tensor `t` after its checks; None stays None (the library refuses a NULL it needs)."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise SblError(SBL_ERR_INVALID_ARG, f"{what}: {name} is {t.dtype}, not one of {dtypes}")
+    if t.get_device() != dev:
+        raise SblError(SBL_ERR_DEVICE, f"{what}: {name} is on {t.device}, the call on CUDA device {dev}")
+    if not t.is_contiguous():
+        raise SblError(SBL_ERR_SHAPE, f"{what}: {name} is not dense")
+    if t.numel() != numel:
+        raise SblError(SBL_ERR_SHAPE, f"{what}: {name} has {t.numel()} elements, not {numel}")
+    return t.data_ptr()
+
+
+def _room(T: _Types, what: str, t, nbytes: int, dev: int):
+    """The address of a uint8 workspace of `nbytes` or more."""
+    return None if t is None else _addr(what, "workspace", t, T.u8, max(t.numel(), nbytes), dev)
+
+
+def _raw_stream(T: _Types, stream, dev: int):
+    if stream is not None:
+        return stream.cuda_stream
+    return T.raw_stream(dev) if T.raw_stream is not None else _stream().value
 
 
 def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h_out=None, xn_out=None, xhat_out=None,
@@ -416,24 +444,22 @@ def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h
     (``xq_out``, ``xscale_out``; ``xhat_out``: the values they stand for).
     x, the stream (residual, h_out) and weight are bf16 or fp32 each; without a
     residual h_out has x's type.  ``status``: a device int32 tensor or None."""
-    a = _Args("sbl_rmsnorm_forward")
-    T = a.torch
-    bf, f32 = T.bfloat16, T.float32
-    any_, n = (bf, f32), t * k
-    xp = a(x, "x", any_, n)
-    flags = SBL_NORM_X_F32 if x.dtype is f32 else 0
-    stream_type = x.dtype if residual is None else residual.dtype
-    if stream_type is f32:
-        flags |= SBL_NORM_STREAM_F32
-    if weight is not None and weight.dtype is f32:
-        flags |= SBL_NORM_W_F32
+    T, me, n = _torch_types(), "sbl_rmsnorm_forward", t * k
+    dev = _device(T, me, "x", x)
+    xp = _addr(me, "x", x, T.float, n, dev)
+    rp = _addr(me, "residual", residual, T.float, n, dev)
+    wp = _addr(me, "weight", weight, T.float, k, dev)
+    stream_type = (x.dtype,) if residual is None else (residual.dtype,)
+    flags = ((SBL_NORM_X_F32 if x.dtype in T.f32 else 0) | (SBL_NORM_STREAM_F32 if stream_type == T.f32 else 0)
+             | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
     code = lib().sbl_rmsnorm_forward(
-        xp, a(residual, "residual", any_, n, True), a(weight, "weight", any_, k, True), t, k, eps, flags,
-        a(h_out, "h_out", (stream_type,), n, True), a(xn_out, "xn_out", (bf,), n, True),
-        a(xhat_out, "xhat_out", (bf,), n, True), a(xq_out, "xq_out", (T.int8,), n, True),
-        a(xscale_out, "xscale_out", (f32,), t, True), a(rstd_out, "rstd_out", (f32,), t, True),
-        a(status, "status", (T.int32,), 1, True), _stream(stream))
-    _check(code, "sbl_rmsnorm_forward")
+        xp, rp, wp, t, k, eps, flags, _addr(me, "h_out", h_out, stream_type, n, dev),
+        _addr(me, "xn_out", xn_out, T.bf16, n, dev), _addr(me, "xhat_out", xhat_out, T.bf16, n, dev),
+        _addr(me, "xq_out", xq_out, T.i8, n, dev), _addr(me, "xscale_out", xscale_out, T.f32, t, dev),
+        _addr(me, "rstd_out", rstd_out, T.f32, t, dev), _addr(me, "status", status, T.i32, 1, dev),
+        _raw_stream(T, stream, dev))
+    if code:
+        raise SblError(code, me)
 
 
 def rmsnorm_backward_workspace_bytes(t: int, k: int) -> int:
@@ -447,26 +473,25 @@ def rmsnorm_backward(h, rstd, dys, t: int, k: int, dh, weight=None, dres=None, d
     are added) and ``dres`` (the residual stream's own gradient or None); dx: a
     bf16 copy of dh or None; dw: fp32 gradient of the weight or None (it needs
     ``workspace``, a uint8 tensor of rmsnorm_backward_workspace_bytes)."""
-    a = _Args("sbl_rmsnorm_backward")
-    T = a.torch
-    bf, f32 = T.bfloat16, T.float32
-    any_, n = (bf, f32), t * k
+    T, me, n = _torch_types(), "sbl_rmsnorm_backward", t * k
     if not 1 <= len(dys) <= 3:
-        a.refuse(SBL_ERR_INVALID_ARG, f"{len(dys)} gradients, not 1 to 3")
-    hp = a(h, "h", any_, n)
-    flags = SBL_NORM_STREAM_F32 if h.dtype is f32 else 0
-    if weight is not None and weight.dtype is f32:
-        flags |= SBL_NORM_W_F32
-    if dys[0] is not None and dys[0].dtype is f32:
-        flags |= SBL_NORM_DY_F32
-    dyp = (_P * 3)(*[a(d, "dys", (f32 if flags & SBL_NORM_DY_F32 else bf,), n) for d in dys])
-    ws = a(workspace, "workspace", (T.uint8,), rmsnorm_backward_workspace_bytes(t, k), True, True) if dw is not None \
-        else None
+        raise SblError(SBL_ERR_INVALID_ARG, f"{me}: {len(dys)} gradients, not 1 to 3")
+    dev = _device(T, me, "h", h)
+    hp, stream_type = _addr(me, "h", h, T.float, n, dev), (h.dtype,)
+    _device(T, me, "dys", dys[0])
+    dy_type = (dys[0].dtype,)
+    flags = ((SBL_NORM_STREAM_F32 if stream_type == T.f32 else 0) | (SBL_NORM_DY_F32 if dy_type == T.f32 else 0)
+             | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
+    if dy_type[0] not in T.float:
+        dy_type = T.float
+    dyp = (_P * 3)(*[_addr(me, "dys", d, dy_type, n, dev) for d in dys])
+    ws = _room(T, me, workspace, rmsnorm_backward_workspace_bytes(t, k), dev) if dw is not None else None
     code = lib().sbl_rmsnorm_backward(
-        hp, a(rstd, "rstd", (f32,), t), a(weight, "weight", any_, k, True), dyp, len(dys),
-        a(dres, "dres", (h.dtype,), n, True), t, k, flags, a(dh, "dh", (h.dtype,), n), a(dx, "dx", (bf,), n, True),
-        a(dw, "dw", (f32,), k, True), ws, _stream(stream))
-    _check(code, "sbl_rmsnorm_backward")
+        hp, _addr(me, "rstd", rstd, T.f32, t, dev), _addr(me, "weight", weight, T.float, k, dev), dyp, len(dys),
+        _addr(me, "dres", dres, stream_type, n, dev), t, k, flags, _addr(me, "dh", dh, stream_type, n, dev),
+        _addr(me, "dx", dx, T.bf16, n, dev), _addr(me, "dw", dw, T.f32, k, dev), ws, _raw_stream(T, stream, dev))
+    if code:
+        raise SblError(code, me)
 
 
 @dataclass
@@ -504,31 +529,31 @@ class AdamWTensors:
     addresses stay fixed: build a new one when a tensor is reallocated."""
 
     def __init__(self, tensors):
-        a = _Args("sbl.AdamWTensors")
-        T = a.torch
-        bf, f32 = T.bfloat16, T.float32
+        T, me = _torch_types(), "sbl.AdamWTensors"
         self.tensors = list(tensors)
         self.count = len(self.tensors)
-        self.device = a.device
         self.array = (sbl_adamw_tensor * max(self.count, 1))()
+        self.device = -1
         for c, p in zip(self.array, self.tensors):
-            if p.w is None or p.grad is None or p.m is None:
-                a.refuse(SBL_ERR_INVALID_ARG, "w, grad or m is missing")
+            if p.w is None or p.grad is None or p.m is None or p.v is None:
+                raise SblError(SBL_ERR_INVALID_ARG, f"{me}: w, grad, m or v is missing")
+            dev = self.device = _device(T, me, "w", p.w)
             n = p.w.numel()
             c.numel = n
-            eight = p.m.dtype is not f32
-            c.flags = ((SBL_ADAMW_GRAD_F32 if p.grad.dtype is f32 else 0) | (SBL_ADAMW_STATE_8BIT if eight else 0)
+            eight = p.m.dtype not in T.f32
+            c.flags = ((SBL_ADAMW_GRAD_F32 if p.grad.dtype in T.f32 else 0) | (SBL_ADAMW_STATE_8BIT if eight else 0)
                        | (0 if p.decay else SBL_ADAMW_NO_DECAY))
-            c.w = a(p.w, "w", (bf,), n)
-            c.grad = a(p.grad, "grad", (bf, f32), n)
-            state = (T.float8_e4m3fn, T.uint8) if eight else (f32,)
-            c.m = a(p.m, "m", state, n)
-            c.v = a(p.v, "v", state, n)
-            c.master = a(p.master, "master", (f32,), n, True)
+            c.w = _addr(me, "w", p.w, T.bf16, n, dev)
+            c.grad = _addr(me, "grad", p.grad, T.float, n, dev)
+            c.m = _addr(me, "m", p.m, T.code8 if eight else T.f32, n, dev)
+            c.v = _addr(me, "v", p.v, T.code8 if eight else T.f32, n, dev)
+            c.master = _addr(me, "master", p.master, T.f32, n, dev)
             if eight:
                 blocks = (n + SBL_ADAMW_BLOCK - 1) // SBL_ADAMW_BLOCK
-                c.m_scale = a(p.m_scale, "m_scale", (f32,), blocks)
-                c.v_scale = a(p.v_scale, "v_scale", (f32,), blocks)
+                if p.m_scale is None or p.v_scale is None:
+                    raise SblError(SBL_ERR_INVALID_ARG, f"{me}: 8-bit states without m_scale or v_scale")
+                c.m_scale = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
+                c.v_scale = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
 
 
 def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95,
@@ -537,15 +562,19 @@ def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, 
     """sbl_adamw_step: one step (the first is ``step`` 1) on every tensor.
     ``lr_dev`` (fp32), ``step_dev`` (int64) and ``grad_scale_dev`` (fp32) are
     device scalars that a captured graph reads at each replay, or None."""
-    a = _Args("sbl_adamw_step")
-    T = a.torch
-    if tensors.device != a.device:
-        a.refuse(SBL_ERR_DEVICE, "the tensors are not on the current CUDA device")
-    params = sbl_adamw_params(lr, beta1, beta2, eps, weight_decay, step,
-                              a(lr_dev, "lr_dev", (T.float32,), 1, True), a(step_dev, "step_dev", (T.int64,), 1, True),
-                              a(grad_scale_dev, "grad_scale_dev", (T.float32,), 1, True))
-    _check(lib().sbl_adamw_step(tensors.array, tensors.count, ctypes.byref(params),
-                                a(status, "status", (T.int32,), 1, True), _stream(stream)), "sbl_adamw_step")
+    T, me = _torch_types(), "sbl_adamw_step"
+    if tensors.count == 0:
+        return
+    dev = tensors.device
+    if dev != T.current_device():
+        raise SblError(SBL_ERR_DEVICE, f"{me}: the tensors are not on the current CUDA device")
+    params = sbl_adamw_params(lr, beta1, beta2, eps, weight_decay, step, _addr(me, "lr_dev", lr_dev, T.f32, 1, dev),
+                              _addr(me, "step_dev", step_dev, T.i64, 1, dev),
+                              _addr(me, "grad_scale_dev", grad_scale_dev, T.f32, 1, dev))
+    code = lib().sbl_adamw_step(tensors.array, tensors.count, ctypes.byref(params),
+                                _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
+    if code:
+        raise SblError(code, me)
 
 
 def linear_ce_workspace_bytes(t: int, v: int, d: int, backward: bool = False) -> int:
@@ -557,15 +586,15 @@ def linear_ce_forward(h, w, targets, t: int, v: int, d: int, loss, lse, workspac
     """sbl_linear_ce_forward: loss[i] = log sum exp(h[i] w^T) - (h[i] w^T)[targets[i]]
     and lse, the logits never in memory.  h: bf16 [t, d], w: bf16 [v, d],
     targets: int64 [t], workspace: uint8, linear_ce_workspace_bytes(t, v, d)."""
-    a = _Args("sbl_linear_ce_forward")
-    T = a.torch
-    bf, f32 = (T.bfloat16,), (T.float32,)
+    T, me = _torch_types(), "sbl_linear_ce_forward"
+    dev = _device(T, me, "h", h)
     code = lib().sbl_linear_ce_forward(
-        a(h, "h", bf, t * d), a(w, "w", bf, v * d), a(targets, "targets", (T.int64,), t), t, v, d, ignore_index,
-        a(loss, "loss", f32, t), a(lse, "lse", f32, t),
-        a(workspace, "workspace", (T.uint8,), linear_ce_workspace_bytes(t, v, d), False, True),
-        a(status, "status", (T.int32,), 1, True), _stream(stream))
-    _check(code, "sbl_linear_ce_forward")
+        _addr(me, "h", h, T.bf16, t * d, dev), _addr(me, "w", w, T.bf16, v * d, dev),
+        _addr(me, "targets", targets, T.i64, t, dev), t, v, d, ignore_index, _addr(me, "loss", loss, T.f32, t, dev),
+        _addr(me, "lse", lse, T.f32, t, dev), _room(T, me, workspace, linear_ce_workspace_bytes(t, v, d), dev),
+        _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
+    if code:
+        raise SblError(code, me)
 
 
 def linear_ce_backward(h, w, targets, lse, dloss, t: int, v: int, d: int, dh, dw, workspace,
@@ -573,17 +602,18 @@ def linear_ce_backward(h, w, targets, lse, dloss, t: int, v: int, d: int, dh, dw
     """sbl_linear_ce_backward: dh (bf16 [t, d]) and dw (bf16 [v, d]) from the
     forward's lse and ``dloss``, fp32 of t elements (each loss's gradient) or of
     one (the same for all).  workspace: linear_ce_workspace_bytes(t, v, d, True)."""
-    a = _Args("sbl_linear_ce_backward")
-    T = a.torch
-    bf, f32 = (T.bfloat16,), (T.float32,)
+    T, me = _torch_types(), "sbl_linear_ce_backward"
+    dev = _device(T, me, "h", h)
     one = dloss is not None and dloss.numel() == 1
     code = lib().sbl_linear_ce_backward(
-        a(h, "h", bf, t * d), a(w, "w", bf, v * d), a(targets, "targets", (T.int64,), t), a(lse, "lse", f32, t),
-        a(dloss, "dloss", f32, 1 if one else t), 0 if one else 1, t, v, d, ignore_index, a(dh, "dh", bf, t * d),
-        a(dw, "dw", bf, v * d),
-        a(workspace, "workspace", (T.uint8,), linear_ce_workspace_bytes(t, v, d, True), False, True),
-        a(status, "status", (T.int32,), 1, True), _stream(stream))
-    _check(code, "sbl_linear_ce_backward")
+        _addr(me, "h", h, T.bf16, t * d, dev), _addr(me, "w", w, T.bf16, v * d, dev),
+        _addr(me, "targets", targets, T.i64, t, dev), _addr(me, "lse", lse, T.f32, t, dev),
+        _addr(me, "dloss", dloss, T.f32, 1 if one else t, dev), 0 if one else 1, t, v, d, ignore_index,
+        _addr(me, "dh", dh, T.bf16, t * d, dev), _addr(me, "dw", dw, T.bf16, v * d, dev),
+        _room(T, me, workspace, linear_ce_workspace_bytes(t, v, d, True), dev),
+        _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
+    if code:
+        raise SblError(code, me)
 
 
 class SparseBitLinear:
