@@ -10,7 +10,10 @@
 // and rstd is the correctly rounded value but for about one row in 10^7, so
 // the int8 codes, which sit behind two roundings, are reproducible.
 //
-// A row belongs to a group of TPR threads, R vectors of 8 elements a thread.
+// A row belongs to W warps (one block, or one warp of a block of four rows),
+// R vectors of 8 elements a lane.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "actq_math.cuh"
@@ -21,6 +24,15 @@ namespace sbl {
 
 namespace {
 
+__device__ __forceinline__ void unpack8(const uint4 a, float (&f)[8]) {
+  const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = __uint_as_float(u[e] << 16);
+    f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+  }
+}
+
 template <bool F32>
 __device__ __forceinline__ void load8(const void* base, int64_t vec, float (&f)[8]) {
   if constexpr (F32) {
@@ -29,13 +41,7 @@ __device__ __forceinline__ void load8(const void* base, int64_t vec, float (&f)[
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   } else {
-    const uint4 a = static_cast<const uint4*>(base)[vec];
-    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(u[e] << 16);
-      f[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-    }
+    unpack8(static_cast<const uint4*>(base)[vec], f);
   }
 }
 
@@ -82,98 +88,121 @@ struct NormParams {
   uint32_t* status;
 };
 
-constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+// Residual types of the forward kernel.
+enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
-// Sum over the row's threads, the same value in each of them.
-template <int TPR, class T>
-__device__ __forceinline__ T row_sum(T v, T* part) {
+// Eight codes as quantise8_fma gives them, and the bf16 values they stand for:
+// the code is at hand as a float (its byte's sum minus 1.5 2^23), so no byte is
+// taken apart again.
+__device__ __forceinline__ uint2 quantise8_values(const uint4 v, const QScale& s, float a_over_127, uint4* values) {
+  const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bytes[8], packed[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = part[0];
-#pragma unroll
-    for (int i = 1; i < TPR / 32; ++i) v += part[i];
+  for (int h = 0; h < 4; ++h) {
+    const float lo = __fmaf_rn(__uint_as_float(words[h] << 16), s.c, 12582912.0f);
+    const float hi = __fmaf_rn(__uint_as_float(words[h] & 0xFFFF0000u), s.c, 12582912.0f);
+    bytes[2 * h] = __float_as_uint(lo), bytes[2 * h + 1] = __float_as_uint(hi);
+    packed[h] = pack2(__fmul_rn(__fsub_rn(lo, 12582912.0f), a_over_127), __fmul_rn(__fsub_rn(hi, 12582912.0f), a_over_127));
   }
-  return v;
+  *values = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+  return make_uint2(__byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040), __byte_perm(bytes[2], bytes[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(bytes[4], bytes[5], 0x0040), __byte_perm(bytes[6], bytes[7], 0x0040), 0x5410));
 }
 
-template <int TPR>
-__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  if constexpr (TPR > 32) {
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = part[0];
-#pragma unroll
-    for (int i = 1; i < TPR / 32; ++i) v = max(v, part[i]);
-  }
-  return v;
-}
+constexpr int kNormMaxWarps = 16;
 
-template <bool XF32, bool HF32, int TPR, int R>
-__global__ void __launch_bounds__(norm_block(TPR)) k_rmsnorm(const NormParams p) {
-  __shared__ double s_sum[norm_block(TPR) / 32];
-  __shared__ uint32_t s_max[norm_block(TPR) / 32];
+template <bool XF32, int RES, int R, bool ONE_WARP>
+__global__ void __launch_bounds__(ONE_WARP ? 128 : kNormMaxWarps * 32, ONE_WARP ? 4 : 1)
+    k_rmsnorm(const NormParams p) {
+  constexpr bool HF32 = RES == kNoRes ? XF32 : RES == kResF32;
+  __shared__ double s_sum[kNormMaxWarps];
+  __shared__ uint32_t s_max[kNormMaxWarps];
   pdl_wait();
   pdl_trigger();
-  constexpr int kRows = norm_block(TPR) / TPR;
-  const int tid = threadIdx.x % TPR;
-  const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
-  if (row >= p.t) return;  // whole warps: with more than one row a block, a row is one warp
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int step = ONE_WARP ? 32 : static_cast<int>(blockDim.x);
+  const int tid = ONE_WARP ? lane : static_cast<int>(threadIdx.x);
+  const int64_t row = ONE_WARP ? int64_t(blockIdx.x) * 4 + warp : int64_t(blockIdx.x);
+  if (row >= p.t) return;  // whole warps, and only where a row is one warp
   const int64_t base = row * p.nvec;
 
-  float h[R][8];
+  // h: fp32, or two bf16 a word
+  float hf[HF32 ? R : 1][8];
+  uint4 hb[HF32 ? 1 : R];
   double ss = 0.0;
+  {
+    float x[R][8], q[RES == kNoRes ? 1 : R][8];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = r * TPR + tid;
-    if (i < p.nvec) {
-      load8<XF32>(p.x, base + i, h[r]);
-      if (p.res != nullptr) {
-        float q[8];
-        load8<HF32>(p.res, base + i, q);
+    for (int r = 0; r < R; ++r) {
+      const int i = r * step + tid;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[r][e] = __fadd_rn(h[r][e], q[e]);
+      for (int e = 0; e < 8; ++e) x[r][e] = 0.0f;
+      if constexpr (RES != kNoRes)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[r][e] = 0.0f;
+      if (i < p.nvec) {
+        load8<XF32>(p.x, base + i, x[r]);
+        if constexpr (RES != kNoRes) load8<RES == kResF32>(p.res, base + i, q[r]);
       }
-    } else {
+    }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[r][e] = 0.0f;
+    for (int r = 0; r < R; ++r) {
+      if constexpr (RES != kNoRes)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[r][e] = __fadd_rn(x[r][e], q[r][e]);
+      if constexpr (HF32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hf[r][e] = x[r][e];
+      } else {
+        hb[r] = pack8(x[r]);
+        unpack8(hb[r], x[r]);
+      }
+      const int i = r * step + tid;
+      if (p.h != nullptr && i < p.nvec) {
+        if constexpr (HF32)
+          store8<true>(p.h, base + i, hf[r]);
+        else
+          static_cast<uint4*>(p.h)[base + i] = hb[r];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double d = x[r][e];
+        ss = fma(d, d, ss);
+      }
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if constexpr (!HF32) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[r][e] = __bfloat162float(__float2bfloat16_rn(h[r][e]));
-    }
-    const int i = r * TPR + tid;
-    if (p.h != nullptr && i < p.nvec) store8<HF32>(p.h, base + i, h[r]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double d = h[r][e];
-      ss = fma(d, d, ss);
-    }
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  if constexpr (!ONE_WARP) {
+    if (lane == 0) s_sum[warp] = ss;
+    __syncthreads();
+    ss = s_sum[0];
+    for (int i = 1; i < step / 32; ++i) ss += s_sum[i];
   }
-  ss = row_sum<TPR>(ss, s_sum);
   const float rstd = inverse_root(fma(ss, p.inv_k, p.eps));
   if (tid == 0) {
     if (p.rstd != nullptr) p.rstd[row] = rstd;
     if (!(ss < __longlong_as_double(0x7FF0000000000000ll))) raise_status(p.status, SBL_STATUS_NONFINITE_X);
   }
-  if (p.xn == nullptr && p.xhat == nullptr && p.xq == nullptr && p.xscale == nullptr) return;
+  const bool quant = p.xhat != nullptr || p.xq != nullptr || p.xscale != nullptr;
+  if (p.xn == nullptr && !quant) return;
 
   uint4 v[R];
   uint32_t m2 = 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = r * TPR + tid;
+    const int i = r * step + tid;
     v[r] = make_uint4(0, 0, 0, 0);
     if (i < p.nvec) {
       float n[8];
+      if constexpr (HF32) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(h[r][e], rstd);
+        for (int e = 0; e < 8; ++e) n[e] = hf[r][e];
+      } else {
+        unpack8(hb[r], n);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(n[e], rstd);
       if (p.w != nullptr) {
         float w[8];
         if (p.w_f32)
@@ -193,46 +222,85 @@ __global__ void __launch_bounds__(norm_block(TPR)) k_rmsnorm(const NormParams p)
   }
   uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
   if (m >= 0x7F80u) raise_status(p.status, SBL_STATUS_NONFINITE_X);
-  if (p.xhat == nullptr && p.xq == nullptr && p.xscale == nullptr) return;
+  if (!quant) return;
 
-  m = row_max<TPR>(m, s_max);
+  m = __reduce_max_sync(0xffffffffu, m);
+  if constexpr (!ONE_WARP) {
+    if (lane == 0) s_max[warp] = m;
+    __syncthreads();
+    m = s_max[0];
+    for (int i = 1; i < step / 32; ++i) m = max(m, s_max[i]);
+  }
   const float ap = fmaxf(__uint_as_float(m << 16), 1e-5f);
   if (tid == 0 && p.xscale != nullptr) p.xscale[row] = ap;
   const QScale qs = make_qscale(ap);
+  if (m == 0) {  // a row of zeros (padding): no division for it
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = r * step + tid;
+      if (i >= p.nvec) break;
+      if (p.xq != nullptr) p.xq[base + i] = make_uint2(0, 0);
+      if (p.xhat != nullptr) p.xhat[base + i] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  if (qs.exact) {  // the clamp or a' >= 2^120: the IEEE division
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+      const int i = r * step + tid;
+      if (i >= p.nvec) break;
+      uint4 u = v[0];  // v[r], without a register array indexed at run time
+#pragma unroll
+      for (int j = 1; j < R; ++j)
+        if (j == r) u = v[j];
+      if (p.xq != nullptr) p.xq[base + i] = quantise8_div(u, ap);
+      if (p.xhat != nullptr) p.xhat[base + i] = dequantise8(u, qs);
+    }
+    return;
+  }
   const float a_over_127 = __fdiv_rn(ap, 127.0f);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = r * TPR + tid;
+    const int i = r * step + tid;
     if (i < p.nvec) {
-      const uint2 c = quantise8(v[r], qs);
+      uint4 values;
+      const uint2 c = quantise8_values(v[r], qs, a_over_127, &values);
       if (p.xq != nullptr) p.xq[base + i] = c;
-      if (p.xhat != nullptr) p.xhat[base + i] = qs.exact ? dequantise8(v[r], qs) : dequant8_fast(c, a_over_127);
+      if (p.xhat != nullptr) p.xhat[base + i] = values;
     }
   }
 }
 
-template <bool XF32, bool HF32, int TPR, int R>
-cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
-  constexpr int rows = norm_block(TPR) / TPR;
-  return launch_pdl(k_rmsnorm<XF32, HF32, TPR, R>, dim3(static_cast<unsigned>((p.t + rows - 1) / rows)),
-                    dim3(norm_block(TPR)), 0, s, p);
+template <bool XF32, int RES, int R>
+cudaError_t launch_norm(const NormParams& p, int warps, cudaStream_t s) {
+  if (warps == 1)
+    return launch_pdl(k_rmsnorm<XF32, RES, R, true>, dim3(static_cast<unsigned>((p.t + 3) / 4)), dim3(128), 0, s, p);
+  return launch_pdl(k_rmsnorm<XF32, RES, R, false>, dim3(static_cast<unsigned>(p.t)), dim3(32 * warps), 0, s, p);
 }
 
-// Threads a row: as few as hold it with four vectors each, for the most rows
-// in flight.
-template <bool XF32, bool HF32>
-cudaError_t pick_norm(const NormParams& p, cudaStream_t s) {
+// Warps a row.  Every lane repeats the row's scalar work (the root, the
+// quantiser's constants), so with enough rows a lane takes up to kLaneVecs
+// vectors, with the number of warps that leaves the fewest lanes idle; with few
+// rows the row's own latency counts and more warps share it.
+constexpr int kLaneVecs = 6;  // more would spill
+
+template <bool XF32, int RES>
+cudaError_t pick_norm(const NormParams& p, int num_sms, cudaStream_t s) {
   const int n = p.nvec;
-  if (n <= 32) return launch_norm<XF32, HF32, 32, 1>(p, s);
-  if (n <= 64) return launch_norm<XF32, HF32, 32, 2>(p, s);
-  if (n <= 96) return launch_norm<XF32, HF32, 32, 3>(p, s);
-  if (n <= 128) return launch_norm<XF32, HF32, 32, 4>(p, s);
-  if (n <= 256) return launch_norm<XF32, HF32, 128, 2>(p, s);
-  if (n <= 384) return launch_norm<XF32, HF32, 128, 3>(p, s);
-  if (n <= 512) return launch_norm<XF32, HF32, 128, 4>(p, s);
-  if (n <= 1024) return launch_norm<XF32, HF32, 512, 2>(p, s);
-  if (n <= 1536) return launch_norm<XF32, HF32, 512, 3>(p, s);
-  return launch_norm<XF32, HF32, 512, 4>(p, s);
+  const bool few = p.t <= 2 * num_sms;
+  const auto vecs = [n](int w) { return (n + 32 * w - 1) / (32 * w); };
+  int warps = few ? std::min((n + 31) / 32, kNormMaxWarps) : (n + 32 * kLaneVecs - 1) / (32 * kLaneVecs);
+  if (!few)
+    for (int w = warps + 1; w <= std::min(warps + 3, kNormMaxWarps); ++w)
+      if (w * vecs(w) < warps * vecs(warps)) warps = w;
+  switch (vecs(warps)) {
+    case 1: return launch_norm<XF32, RES, 1>(p, warps, s);
+    case 2: return launch_norm<XF32, RES, 2>(p, warps, s);
+    case 3: return launch_norm<XF32, RES, 3>(p, warps, s);
+    case 4: return launch_norm<XF32, RES, 4>(p, warps, s);
+    case 5: return launch_norm<XF32, RES, 5>(p, warps, s);
+    default: return launch_norm<XF32, RES, 6>(p, warps, s);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -442,7 +510,7 @@ cudaError_t pick_norm_bwd(const NormBwdParams& p, float* dw, int num_sms, cudaSt
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s) {
   NormParams p;
   p.x = a.x, p.res = a.residual, p.w = a.weight;
   p.t = a.t, p.nvec = static_cast<int>(a.k / 8);
@@ -451,10 +519,10 @@ cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t s) {
   p.h = a.h;
   p.xn = static_cast<uint4*>(a.xn), p.xhat = static_cast<uint4*>(a.xhat), p.xq = reinterpret_cast<uint2*>(a.xq);
   p.xscale = a.xscale, p.rstd = a.rstd, p.status = a.status;
-  const bool xf = (a.flags & SBL_NORM_X_F32) != 0u;
-  const bool hf = a.residual != nullptr ? (a.flags & SBL_NORM_STREAM_F32) != 0u : xf;
-  if (xf) return hf ? pick_norm<true, true>(p, s) : pick_norm<true, false>(p, s);
-  return hf ? pick_norm<false, true>(p, s) : pick_norm<false, false>(p, s);
+  const bool xf = (a.flags & SBL_NORM_X_F32) != 0u, rf = (a.flags & SBL_NORM_STREAM_F32) != 0u;
+  if (a.residual == nullptr) return xf ? pick_norm<true, kNoRes>(p, num_sms, s) : pick_norm<false, kNoRes>(p, num_sms, s);
+  if (rf) return xf ? pick_norm<true, kResF32>(p, num_sms, s) : pick_norm<false, kResF32>(p, num_sms, s);
+  return xf ? pick_norm<true, kResBf16>(p, num_sms, s) : pick_norm<false, kResBf16>(p, num_sms, s);
 }
 
 int64_t rmsnorm_bwd_max_blocks(int64_t t) { return t < kNormBwdMaxBlocks ? t : kNormBwdMaxBlocks; }

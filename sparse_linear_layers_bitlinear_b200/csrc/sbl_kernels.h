@@ -141,7 +141,7 @@ struct NormArgs {
   float *xscale, *rstd;
   uint32_t* status;
 };
-cudaError_t launch_rmsnorm(const NormArgs& a, cudaStream_t s);
+cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s);
 
 struct NormBwdArgs {
   const void* h;

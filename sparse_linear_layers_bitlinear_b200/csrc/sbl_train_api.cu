@@ -57,7 +57,7 @@ sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* 
   if (st != SBL_OK) return st;
   const NormArgs a{x, residual, weight, t, k, eps, flags, h_out, xn_out, xhat_out, xq_out, xscale_out, rstd_out,
                    status_dev};
-  return code(launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)));
+  return code(launch_rmsnorm(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t sbl_rmsnorm_backward_workspace_bytes(int64_t t, int64_t k) {
