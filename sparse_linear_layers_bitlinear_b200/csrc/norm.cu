@@ -91,216 +91,355 @@ struct NormParams {
 // Residual types of the forward kernel.
 enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
+// Two fp32 values in a register pair: sm_100's packed fp32 instructions, each
+// half rounded as the scalar ones do.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 unpack2(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+  const float2 f = halves(v);
+  return pack2(f.x, f.y);
+}
+
+// The larger magnitudes of two pairs of bf16 values; a NaN stays.
+__device__ __forceinline__ uint32_t top2(uint32_t top, uint32_t w) {
+  const __nv_bfloat162 a = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
+  return *reinterpret_cast<const uint32_t*>(&a);
+}
+
+// Eight elements as they lie in memory.
+template <bool F32>
+struct Raw {
+  uint4 w[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t vec) {
+    const uint4* src = static_cast<const uint4*>(base) + (F32 ? 2 : 1) * vec;
+    w[0] = src[0];
+    if constexpr (F32) w[1] = src[1];
+  }
+  __device__ __forceinline__ void zero() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (F32) w[1] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void unpack(f32x2 (&f)[4]) const {
+    if constexpr (F32) {
+      f[0] = pair(__uint_as_float(w[0].x), __uint_as_float(w[0].y));
+      f[1] = pair(__uint_as_float(w[0].z), __uint_as_float(w[0].w));
+      f[2] = pair(__uint_as_float(w[1].x), __uint_as_float(w[1].y));
+      f[3] = pair(__uint_as_float(w[1].z), __uint_as_float(w[1].w));
+    } else {
+      f[0] = unpack2(w[0].x), f[1] = unpack2(w[0].y), f[2] = unpack2(w[0].z), f[3] = unpack2(w[0].w);
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
+  return make_uint4(pack2(f[0]), pack2(f[1]), pack2(f[2]), pack2(f[3]));
+}
+
 // Eight codes as quantise8_fma gives them, and the bf16 values they stand for:
 // the code is at hand as a float (its byte's sum minus 1.5 2^23), so no byte is
 // taken apart again.
-__device__ __forceinline__ uint2 quantise8_values(const uint4 v, const QScale& s, float a_over_127, uint4* values) {
+__device__ __forceinline__ uint2 quantise8_values(const uint4 v, float c, float a_over_127, uint4* values) {
   const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-  uint32_t bytes[8], packed[4];
+  const f32x2 c2 = pair(c, c), a2 = pair(a_over_127, a_over_127), up = pair(12582912.0f, 12582912.0f),
+              down = pair(-12582912.0f, -12582912.0f);
+  uint32_t bytes[4], packed[4];
 #pragma unroll
   for (int h = 0; h < 4; ++h) {
-    const float lo = __fmaf_rn(__uint_as_float(words[h] << 16), s.c, 12582912.0f);
-    const float hi = __fmaf_rn(__uint_as_float(words[h] & 0xFFFF0000u), s.c, 12582912.0f);
-    bytes[2 * h] = __float_as_uint(lo), bytes[2 * h + 1] = __float_as_uint(hi);
-    packed[h] = pack2(__fmul_rn(__fsub_rn(lo, 12582912.0f), a_over_127), __fmul_rn(__fsub_rn(hi, 12582912.0f), a_over_127));
+    const f32x2 f = fma2(unpack2(words[h]), c2, up);
+    const float2 b = halves(f);
+    bytes[h] = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+    packed[h] = pack2(mul2(add2(f, down), a2));
   }
   *values = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-  return make_uint2(__byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040), __byte_perm(bytes[2], bytes[3], 0x0040), 0x5410),
-                    __byte_perm(__byte_perm(bytes[4], bytes[5], 0x0040), __byte_perm(bytes[6], bytes[7], 0x0040), 0x5410));
+  return make_uint2(__byte_perm(bytes[0], bytes[1], 0x5410), __byte_perm(bytes[2], bytes[3], 0x5410));
 }
 
-constexpr int kNormMaxWarps = 16;
+constexpr int kNormMaxWarps = 16;  // of a row with few rows at hand
+constexpr int kNormRowWarps = 12;  // of a row otherwise (with a residual: 168 registers a thread at most)
 
-template <bool XF32, int RES, int R, bool ONE_WARP>
-__global__ void __launch_bounds__(ONE_WARP ? 128 : kNormMaxWarps * 32, ONE_WARP ? 4 : 1)
-    k_rmsnorm(const NormParams p) {
+// A block walks rows with a stride of the grid; the next row's loads are on
+// their way while a row is computed.  The weight lies in shared memory as fp32
+// for all of the block's rows, or (FEW: a block has one row) is loaded beside it.
+template <bool XF32, int RES, int R, bool ONE_WARP, bool FEW>
+__global__ void __launch_bounds__(ONE_WARP ? 128 : FEW || RES == kNoRes ? kNormMaxWarps * 32 : kNormRowWarps * 32, 1) k_rmsnorm(const NormParams p) {
   constexpr bool HF32 = RES == kNoRes ? XF32 : RES == kResF32;
-  __shared__ double s_sum[kNormMaxWarps];
-  __shared__ uint32_t s_max[kNormMaxWarps];
+  __shared__ double s_sum[2][kNormMaxWarps];
+  __shared__ uint32_t s_max[2][kNormMaxWarps];
+  extern __shared__ float4 s_w[];  // [k / 4], without FEW
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warps = ONE_WARP ? 1 : static_cast<int>(blockDim.x) / 32;
+  const bool first = ONE_WARP ? lane == 0 : threadIdx.x == 0;
+  // a warp's vectors lie side by side: their offsets are constants
+  const int at = (ONE_WARP ? 0 : warp * R * 32) + lane;
+  constexpr int kRows = ONE_WARP ? 4 : 1;
+  int64_t row = ONE_WARP ? int64_t(blockIdx.x) * kRows + warp : int64_t(blockIdx.x);
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int step = ONE_WARP ? 32 : static_cast<int>(blockDim.x);
-  const int tid = ONE_WARP ? lane : static_cast<int>(threadIdx.x);
-  const int64_t row = ONE_WARP ? int64_t(blockIdx.x) * 4 + warp : int64_t(blockIdx.x);
-  if (row >= p.t) return;  // whole warps, and only where a row is one warp
-  const int64_t base = row * p.nvec;
 
-  // h: fp32, or two bf16 a word
-  float hf[HF32 ? R : 1][8];
-  uint4 hb[HF32 ? 1 : R];
-  double ss = 0.0;
-  {
-    float x[R][8], q[RES == kNoRes ? 1 : R][8];
+  Raw<XF32> x[R];
+  Raw<RES == kResF32> q[RES == kNoRes ? 1 : R];
+  const auto fetch = [&](int64_t next) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = r * step + tid;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[r][e] = 0.0f;
-      if constexpr (RES != kNoRes)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[r][e] = 0.0f;
+      const int i = at + r * 32;
       if (i < p.nvec) {
-        load8<XF32>(p.x, base + i, x[r]);
-        if constexpr (RES != kNoRes) load8<RES == kResF32>(p.res, base + i, q[r]);
+        x[r].load(p.x, next * p.nvec + at + r * 32);
+        if constexpr (RES != kNoRes) q[r].load(p.res, next * p.nvec + at + r * 32);
       }
     }
+  };
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if constexpr (RES != kNoRes)
+  for (int r = 0; r < R; ++r) {  // lanes past the row's end hold zeros throughout
+    x[r].zero();
+    if constexpr (RES != kNoRes) q[r].zero();
+  }
+  if (row < p.t) fetch(row);
+  f32x2 w[FEW ? R : 1][4];
+  if (p.w != nullptr) {
+    if constexpr (FEW) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[r][e] = __fadd_rn(x[r][e], q[r][e]);
-      if constexpr (HF32) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) hf[r][e] = x[r][e];
-      } else {
-        hb[r] = pack8(x[r]);
-        unpack8(hb[r], x[r]);
+      for (int r = 0; r < R; ++r) {
+        const int i = at + r * 32;
+        if (i >= p.nvec) continue;
+        if (p.w_f32) {
+          Raw<true> u;
+          u.load(p.w, i);
+          u.unpack(w[r]);
+        } else {
+          Raw<false> u;
+          u.load(p.w, i);
+          u.unpack(w[r]);
+        }
       }
-      const int i = r * step + tid;
-      if (p.h != nullptr && i < p.nvec) {
-        if constexpr (HF32)
-          store8<true>(p.h, base + i, hf[r]);
+    } else {
+      for (int i = threadIdx.x; i < p.nvec; i += blockDim.x) {
+        float f[8];
+        if (p.w_f32)
+          load8<true>(p.w, i, f);
         else
-          static_cast<uint4*>(p.h)[base + i] = hb[r];
+          load8<false>(p.w, i, f);
+        s_w[2 * i] = make_float4(f[0], f[1], f[2], f[3]);
+        s_w[2 * i + 1] = make_float4(f[4], f[5], f[6], f[7]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double d = x[r][e];
-        ss = fma(d, d, ss);
-      }
+      __syncthreads();
     }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if constexpr (!ONE_WARP) {
-    if (lane == 0) s_sum[warp] = ss;
-    __syncthreads();
-    ss = s_sum[0];
-    for (int i = 1; i < step / 32; ++i) ss += s_sum[i];
-  }
-  const float rstd = inverse_root(fma(ss, p.inv_k, p.eps));
-  if (tid == 0) {
-    if (p.rstd != nullptr) p.rstd[row] = rstd;
-    if (!(ss < __longlong_as_double(0x7FF0000000000000ll))) raise_status(p.status, SBL_STATUS_NONFINITE_X);
   }
   const bool quant = p.xhat != nullptr || p.xq != nullptr || p.xscale != nullptr;
-  if (p.xn == nullptr && !quant) return;
 
-  uint4 v[R];
-  uint32_t m2 = 0;
+  for (int parity = 0; row < p.t; parity ^= 1) {
+    const int64_t base = row * p.nvec + at, next = row + int64_t(gridDim.x) * kRows;
+    f32x2 h[R][4];
+    double ss[2] = {0.0, 0.0};
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = r * step + tid;
-    v[r] = make_uint4(0, 0, 0, 0);
-    if (i < p.nvec) {
-      float n[8];
+    for (int r = 0; r < R; ++r) {
+      const int i = at + r * 32;
+      x[r].unpack(h[r]);
+      if constexpr (RES != kNoRes) {
+        f32x2 u[4];
+        q[r].unpack(u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[r][e] = add2(h[r][e], u[e]);
+      }
       if constexpr (HF32) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = hf[r][e];
+        if (p.h != nullptr && i < p.nvec) {
+          const float2 a = halves(h[r][0]), b = halves(h[r][1]), c = halves(h[r][2]), d = halves(h[r][3]);
+          float4* dst = static_cast<float4*>(p.h) + 2 * (base + r * 32);
+          dst[0] = make_float4(a.x, a.y, b.x, b.y);
+          dst[1] = make_float4(c.x, c.y, d.x, d.y);
+        }
+      } else if constexpr (RES != kNoRes || XF32) {
+        const uint4 b = pack8(h[r]);
+        if (p.h != nullptr && i < p.nvec) static_cast<uint4*>(p.h)[base + r * 32] = b;
+        h[r][0] = unpack2(b.x), h[r][1] = unpack2(b.y), h[r][2] = unpack2(b.z), h[r][3] = unpack2(b.w);
       } else {
-        unpack8(hb[r], n);
+        if (p.h != nullptr && i < p.nvec) static_cast<uint4*>(p.h)[base + r * 32] = x[r].w[0];
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(n[e], rstd);
-      if (p.w != nullptr) {
-        float w[8];
-        if (p.w_f32)
-          load8<true>(p.w, i, w);
-        else
-          load8<false>(p.w, i, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) n[e] = __fmul_rn(n[e], w[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = halves(h[r][e]);
+        const double a = f.x, b = f.y;
+        ss[0] = fma(a, a, ss[0]);
+        ss[1] = fma(b, b, ss[1]);
       }
-      v[r] = pack8(n);
-      if (p.xn != nullptr) p.xn[base + i] = v[r];
     }
-    m2 = __vmaxu2(m2, v[r].x & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[r].y & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[r].z & 0x7FFF7FFFu);
-    m2 = __vmaxu2(m2, v[r].w & 0x7FFF7FFFu);
-  }
-  uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-  if (m >= 0x7F80u) raise_status(p.status, SBL_STATUS_NONFINITE_X);
-  if (!quant) return;
-
-  m = __reduce_max_sync(0xffffffffu, m);
-  if constexpr (!ONE_WARP) {
-    if (lane == 0) s_max[warp] = m;
-    __syncthreads();
-    m = s_max[0];
-    for (int i = 1; i < step / 32; ++i) m = max(m, s_max[i]);
-  }
-  const float ap = fmaxf(__uint_as_float(m << 16), 1e-5f);
-  if (tid == 0 && p.xscale != nullptr) p.xscale[row] = ap;
-  const QScale qs = make_qscale(ap);
-  if (m == 0) {  // a row of zeros (padding): no division for it
+    if (!FEW && next < p.t) fetch(next);
+    double sum = ss[0] + ss[1];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = r * step + tid;
-      if (i >= p.nvec) break;
-      if (p.xq != nullptr) p.xq[base + i] = make_uint2(0, 0);
-      if (p.xhat != nullptr) p.xhat[base + i] = make_uint4(0, 0, 0, 0);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if constexpr (!ONE_WARP) {
+      if (lane == 0) s_sum[parity][warp] = sum;
+      __syncthreads();
+      sum = s_sum[parity][0];
+      for (int i = 1; i < warps; ++i) sum += s_sum[parity][i];
     }
-    return;
-  }
-  if (qs.exact) {  // the clamp or a' >= 2^120: the IEEE division
+    const float rstd = inverse_root(fma(sum, p.inv_k, p.eps));
+    if (first) {
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+      if (!(sum < __longlong_as_double(0x7FF0000000000000ll))) raise_status(p.status, SBL_STATUS_NONFINITE_X);
+    }
+    if (p.xn != nullptr || quant) {
+      uint4 v[R];
+      uint32_t m2 = 0;
+      const f32x2 rstd2 = pair(rstd, rstd);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int i = at + r * 32;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[r][e] = mul2(h[r][e], rstd2);
+        if (p.w != nullptr && i < p.nvec) {
+          if constexpr (FEW) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[r][e] = mul2(h[r][e], w[r][e]);
+          } else {
+            const float4 a = s_w[2 * i], b = s_w[2 * i + 1];
+            h[r][0] = mul2(h[r][0], pair(a.x, a.y)), h[r][1] = mul2(h[r][1], pair(a.z, a.w));
+            h[r][2] = mul2(h[r][2], pair(b.x, b.y)), h[r][3] = mul2(h[r][3], pair(b.z, b.w));
+          }
+        }
+        v[r] = pack8(h[r]);
+        if (p.xn != nullptr && i < p.nvec) p.xn[base + r * 32] = v[r];
+        m2 = top2(m2, v[r].x);
+        m2 = top2(m2, v[r].y);
+        m2 = top2(m2, v[r].z);
+        m2 = top2(m2, v[r].w);
+      }
+      uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+      if (m >= 0x7F80u) raise_status(p.status, SBL_STATUS_NONFINITE_X);
+      if (quant) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if constexpr (!ONE_WARP) {
+          if (lane == 0) s_max[parity][warp] = m;
+          __syncthreads();
+          m = s_max[parity][0];
+          for (int i = 1; i < warps; ++i) m = max(m, s_max[parity][i]);
+        }
+        const float ap = fmaxf(__uint_as_float(m << 16), 1e-5f);
+        if (first && p.xscale != nullptr) p.xscale[row] = ap;
+        const QScale qs = make_qscale(ap);
+        const bool zeros = m == 0;  // padding: no division for it
+        const float a_over_127 = __fdiv_rn(ap, 127.0f);
+        if (qs.exact && !zeros) {  // the clamp or a' >= 2^120: the IEEE division
 #pragma unroll 1
-    for (int r = 0; r < R; ++r) {
-      const int i = r * step + tid;
-      if (i >= p.nvec) break;
-      uint4 u = v[0];  // v[r], without a register array indexed at run time
+          for (int r = 0; r < R; ++r) {
+            const int i = at + r * 32;
+            if (i >= p.nvec) break;
+            uint4 u = v[0];  // v[r], without a register array indexed at run time
 #pragma unroll
-      for (int j = 1; j < R; ++j)
-        if (j == r) u = v[j];
-      if (p.xq != nullptr) p.xq[base + i] = quantise8_div(u, ap);
-      if (p.xhat != nullptr) p.xhat[base + i] = dequantise8(u, qs);
-    }
-    return;
-  }
-  const float a_over_127 = __fdiv_rn(ap, 127.0f);
+            for (int j = 1; j < R; ++j)
+              if (j == r) u = v[j];
+            if (p.xq != nullptr) p.xq[base + r * 32] = quantise8_div(u, ap);
+            if (p.xhat != nullptr) p.xhat[base + r * 32] = dequantise8(u, qs);
+          }
+        } else {  // one multiply-add a code; zeros give zeros
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int i = r * step + tid;
-    if (i < p.nvec) {
-      uint4 values;
-      const uint2 c = quantise8_values(v[r], qs, a_over_127, &values);
-      if (p.xq != nullptr) p.xq[base + i] = c;
-      if (p.xhat != nullptr) p.xhat[base + i] = values;
+          for (int r = 0; r < R; ++r) {
+            const int i = at + r * 32;
+            if (i < p.nvec) {
+              uint4 values;
+              const uint2 c = quantise8_values(v[r], qs.c, a_over_127, &values);
+              if (p.xq != nullptr) p.xq[base + r * 32] = c;
+              if (p.xhat != nullptr) p.xhat[base + r * 32] = values;
+            }
+          }
+        }
+      }
     }
+    if (FEW) break;
+    row = next;
   }
+}
+
+template <bool XF32, int RES, int R, bool ONE_WARP, bool FEW>
+cudaError_t launch_norm(const NormParams& p, int warps, int num_sms, cudaStream_t s) {
+  constexpr int rows = ONE_WARP ? 4 : 1;
+  const int threads = ONE_WARP ? 128 : 32 * warps;
+  const size_t smem = !FEW && p.w != nullptr ? size_t(p.nvec) * 32 : 0;
+  int64_t blocks = (p.t + rows - 1) / rows;
+  if constexpr (!FEW) {
+    // one wave of blocks, each with its share of the rows
+    int fit = 0;
+    cudaError_t e = cudaSuccess;
+    if (smem > 48 * 1024)
+      e = cudaFuncSetAttribute(k_rmsnorm<XF32, RES, R, ONE_WARP, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(smem));
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k_rmsnorm<XF32, RES, R, ONE_WARP, FEW>, threads, smem);
+    if (e != cudaSuccess) return e;
+    blocks = std::min<int64_t>(blocks, int64_t(std::max(fit, 1)) * num_sms);
+  }
+  return launch_pdl(k_rmsnorm<XF32, RES, R, ONE_WARP, FEW>, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, s,
+                    p);
 }
 
 template <bool XF32, int RES, int R>
-cudaError_t launch_norm(const NormParams& p, int warps, cudaStream_t s) {
-  if (warps == 1)
-    return launch_pdl(k_rmsnorm<XF32, RES, R, true>, dim3(static_cast<unsigned>((p.t + 3) / 4)), dim3(128), 0, s, p);
-  return launch_pdl(k_rmsnorm<XF32, RES, R, false>, dim3(static_cast<unsigned>(p.t)), dim3(32 * warps), 0, s, p);
+cudaError_t launch_norm(const NormParams& p, int warps, bool few, int num_sms, cudaStream_t s) {
+  if constexpr (R <= 4)
+    if (few) return launch_norm<XF32, RES, R, false, true>(p, warps, num_sms, s);
+  if (warps == 1) return launch_norm<XF32, RES, R, true, false>(p, warps, num_sms, s);
+  return launch_norm<XF32, RES, R, false, false>(p, warps, num_sms, s);
 }
 
-// Warps a row.  Every lane repeats the row's scalar work (the root, the
-// quantiser's constants), so with enough rows a lane takes up to kLaneVecs
-// vectors, with the number of warps that leaves the fewest lanes idle; with few
-// rows the row's own latency counts and more warps share it.
-constexpr int kLaneVecs = 6;  // more would spill
-
+// Warps a row and vectors a lane.  Every warp repeats the row's scalar work (the
+// root, the quantiser's constants: some 200 instructions).  Without a residual
+// that issue is the bound and a lane takes many vectors (8192 x 6912 in bf16:
+// 7 a lane 50 us, 6: 56, 3: 65); with one, more bytes arrive for the same
+// arithmetic and more rows in flight count (4096 x 2560, fp32 on a bf16 stream:
+// 2 a lane 19.3 us, 3: 20.2, 5: 19.9; 8192 x 4096 in bf16: 2 a lane 50 us, 4: 57).
+// Up to three vectors less where that leaves fewer lanes idle.  With few rows the row's
+// own latency counts and more warps share it (one row of 2560: 2.3 against 3.4 us).
 template <bool XF32, int RES>
 cudaError_t pick_norm(const NormParams& p, int num_sms, cudaStream_t s) {
   const int n = p.nvec;
   const bool few = p.t <= 2 * num_sms;
-  const auto vecs = [n](int w) { return (n + 32 * w - 1) / (32 * w); };
-  int warps = few ? std::min((n + 31) / 32, kNormMaxWarps) : (n + 32 * kLaneVecs - 1) / (32 * kLaneVecs);
-  if (!few)
-    for (int w = warps + 1; w <= std::min(warps + 3, kNormMaxWarps); ++w)
-      if (w * vecs(w) < warps * vecs(warps)) warps = w;
-  switch (vecs(warps)) {
-    case 1: return launch_norm<XF32, RES, 1>(p, warps, s);
-    case 2: return launch_norm<XF32, RES, 2>(p, warps, s);
-    case 3: return launch_norm<XF32, RES, 3>(p, warps, s);
-    case 4: return launch_norm<XF32, RES, 4>(p, warps, s);
-    case 5: return launch_norm<XF32, RES, 5>(p, warps, s);
-    default: return launch_norm<XF32, RES, 6>(p, warps, s);
+  const auto up = [](int a, int b) { return (a + b - 1) / b; };
+  int warps = std::min(up(n, 32), kNormMaxWarps);
+  if (!few) {
+    const int most = std::max(RES != kNoRes ? 2 : XF32 ? 5 : 7, up(n, 32 * kNormRowWarps));
+    warps = up(n, 32 * most);
+    for (int r = most - 1; r >= std::max(most - 3, 1); --r) {
+      const int w = up(n, 32 * r);
+      if (w <= kNormRowWarps && w * up(n, 32 * w) < warps * up(n, 32 * warps)) warps = w;
+    }
   }
+  switch (up(n, 32 * warps)) {
+    case 1: return launch_norm<XF32, RES, 1>(p, warps, few, num_sms, s);
+    case 2: return launch_norm<XF32, RES, 2>(p, warps, few, num_sms, s);
+    case 3: return launch_norm<XF32, RES, 3>(p, warps, few, num_sms, s);
+    case 4: return launch_norm<XF32, RES, 4>(p, warps, few, num_sms, s);
+    case 5: return launch_norm<XF32, RES, 5>(p, warps, few, num_sms, s);
+    case 6: return launch_norm<XF32, RES, 6>(p, warps, few, num_sms, s);
+    default: break;
+  }
+  if constexpr (!XF32 && RES == kNoRes) return launch_norm<XF32, RES, 7>(p, warps, few, num_sms, s);
+  return cudaErrorInvalidValue;  // not reached: k is at most SBL_NORM_MAX_K
 }
 
 // ---------------------------------------------------------------------------
