@@ -50,21 +50,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-}
-
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, int64_t vec, const float (&f)[8]) {
-  if constexpr (F32) {
-    float4* dst = static_cast<float4*>(base) + 2 * vec;
-    dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-    dst[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    static_cast<uint4*>(base)[vec] = pack8(f);
-  }
-}
-
 // RN_fp32(1 / sqrt(a)): the fp32 reciprocal root and two Newton steps in fp64
 // (relative error far below fp64's 2^-53 of the exact step), one rounding.
 __device__ __forceinline__ float inverse_root(double a) {
@@ -445,10 +430,14 @@ cudaError_t pick_norm(const NormParams& p, int num_sms, cudaStream_t s) {
 // ---------------------------------------------------------------------------
 // Backward: g = sum dy, n = h rstd, c = mean(w g n),
 //   dh = dres + rstd (w g - n c),   dw = sum over rows of g n.
-// A group of threads walks rows with a fixed stride and keeps its columns'
-// share of dw in registers; the groups of a block add theirs in shared memory
-// in a fixed order, one row of partial sums a block goes to the workspace,
-// and a second launch adds those, in a fixed order too.
+// A group of warps walks rows with a fixed stride and keeps its columns' share
+// of dw in registers.  Up to five arrays are read for one written, so the
+// loads in flight decide the rate: each thread copies its own vectors of the
+// rows to come into its own slots of shared memory (cp.async, a ring of
+// `depth` rows a group), which costs no registers and needs no barrier, since
+// no other thread reads them.  The groups of a block add their dw in shared
+// memory in a fixed order, one row of partial sums a block goes to the
+// workspace, and a second launch adds those, in a fixed order too.
 // ---------------------------------------------------------------------------
 struct NormBwdParams {
   const void* h;
@@ -461,136 +450,290 @@ struct NormBwdParams {
   int nvec;
   float inv_k;
   int w_f32;
+  int warps, groups;  // warps a row, rows a block at a time
+  int depth, words;   // rows of the ring (1 to 3), 16-byte words a thread and row
   void* dh;
-  uint4* dx;
+  void* dx;
   float* part;  // [gridDim.x][k], or nullptr without dw
 };
 
-constexpr int kNormBwdBlock(int tpr) { return tpr < 128 ? 256 : 512; }
+constexpr int kNormBwdThreads = 640;
 
-// The row's threads wait for each other (its own barrier for each group).
-template <int TPR>
-__device__ __forceinline__ void group_sync(int group) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* gmem) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem)), "l"(gmem), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool HF32, bool DF32, int TPR, int R>
-__global__ void __launch_bounds__(kNormBwdBlock(TPR), 1) k_rmsnorm_bwd(const NormBwdParams p) {
-  constexpr int kBlock = kNormBwdBlock(TPR), kGroups = kBlock / TPR, kWarps = TPR / 32;
-  __shared__ float s_part[2][kGroups][kWarps];
-  __shared__ float4 s_dw[kGroups > 1 ? TPR * R * 2 : 1];
+// The eight elements of a lane in a run of 256.  Where an array is fp32 they are
+// two quads 128 elements apart, so that the warp's 16-byte accesses lie side by
+// side (asynchronous copies do not pass through L1: two accesses to the halves
+// of a sector would fetch it twice); with bf16 alone they are eight in a row.
+template <bool QUADS>
+__device__ __forceinline__ int64_t lane_element(int lane) {
+  return QUADS ? 4 * lane : 8 * lane;
+}
+
+// `in`: which of the lane's quads lie in the row (without QUADS both or none).
+template <bool F32, bool QUADS>
+__device__ __forceinline__ void copy8_async(uint4* dst, const void* base, int64_t el, bool in0, bool in1) {
+  const float* f = static_cast<const float*>(base) + el;
+  const uint16_t* h = static_cast<const uint16_t*>(base) + el;
+  if constexpr (F32) {
+    if (in0) copy_async<16>(dst, f);
+    if (in1) copy_async<16>(dst + 32, f + 128);
+  } else if constexpr (QUADS) {
+    if (in0) copy_async<8>(dst, h);
+    if (in1) copy_async<8>(reinterpret_cast<uint2*>(dst) + 1, h + 128);
+  } else {
+    if (in0) copy_async<16>(dst, h);
+  }
+}
+
+template <bool F32, bool QUADS>
+__device__ __forceinline__ Raw<F32> load8_at(const void* base, int64_t el, bool in0, bool in1) {
+  const float* f = static_cast<const float*>(base) + el;
+  const uint16_t* h = static_cast<const uint16_t*>(base) + el;
+  Raw<F32> u;
+  u.zero();
+  if constexpr (F32) {
+    if (in0) u.w[0] = *reinterpret_cast<const uint4*>(f);
+    if (in1) u.w[1] = *reinterpret_cast<const uint4*>(f + (QUADS ? 128 : 4));
+  } else if constexpr (QUADS) {
+    uint2 a = make_uint2(0, 0), b = make_uint2(0, 0);
+    if (in0) a = *reinterpret_cast<const uint2*>(h);
+    if (in1) b = *reinterpret_cast<const uint2*>(h + 128);
+    u.w[0] = make_uint4(a.x, a.y, b.x, b.y);
+  } else {
+    if (in0) u.w[0] = *reinterpret_cast<const uint4*>(h);
+  }
+  return u;
+}
+
+template <bool QUADS>
+__device__ __forceinline__ void store8_bf16(void* base, int64_t el, const uint4 b, bool in0, bool in1) {
+  uint16_t* dst = static_cast<uint16_t*>(base) + el;
+  if constexpr (QUADS) {
+    if (in0) *reinterpret_cast<uint2*>(dst) = make_uint2(b.x, b.y);
+    if (in1) *reinterpret_cast<uint2*>(dst + 128) = make_uint2(b.z, b.w);
+  } else {
+    if (in0) *reinterpret_cast<uint4*>(dst) = b;
+  }
+}
+
+template <bool HF32, bool DF32, int R, bool RING>
+__global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_bwd(const NormBwdParams p) {
+  constexpr int HW = HF32 ? 2 : 1, DW = DF32 ? 2 : 1;
+  constexpr bool QUADS = HF32 || DF32;
+  extern __shared__ uint4 s_ring[];
+  __shared__ float s_part[2][kNormBwdThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = warp / p.warps, k = 8 * p.nvec;
+  const int at = (warp - group * p.warps) * R * 256 + (QUADS ? 4 : 8) * lane;
+  const int64_t first = blockIdx.x + int64_t(group) * gridDim.x, stride = int64_t(p.groups) * gridDim.x;
+  bool in0[R], in1[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) in0[r] = at + r * 256 < k, in1[r] = at + r * 256 + (QUADS ? 128 : 0) < k;
   pdl_wait();
   pdl_trigger();
-  const int group = threadIdx.x / TPR, tid = threadIdx.x % TPR, lane = threadIdx.x & 31, warp = tid >> 5;
-  float acc[R][8];
+
+  // A warp's slot holds the words of its part of a row, 32 lanes each: h, dres,
+  // the gradients, R runs of each; so every word has a constant offset.
+  constexpr int kRes = R * HW, kDy = 2 * R * HW, kOne = R * DW;
+  uint4* const mine = s_ring + warp * p.depth * p.words * 32 + lane;
+  const int slot_step = p.words * 32;
+  const auto fetch = [&](int64_t row, uint4* dst) {
+    const int64_t el = row * k + at;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      copy8_async<HF32, QUADS>(dst + r * HW * 32, p.h, el + r * 256, in0[r], in1[r]);
+      if (p.dres != nullptr)
+        copy8_async<HF32, QUADS>(dst + (kRes + r * HW) * 32, p.dres, el + r * 256, in0[r], in1[r]);
+#pragma unroll
+      for (int d = 0; d < 3; ++d)
+        if (d < p.ndy)
+          copy8_async<DF32, QUADS>(dst + (kDy + d * kOne + r * DW) * 32, p.dy[d], el + r * 256, in0[r], in1[r]);
+    }
+  };
+  // Run r of an array: out of the slot (its word), or (RING false) out of memory.
+  const auto h_at = [&](const uint4* src, int word, const void* base, int64_t el, int r) {
+    if constexpr (RING) {
+      Raw<HF32> u;
+#pragma unroll
+      for (int j = 0; j < HW; ++j) u.w[j] = src[(word + r * HW + j) * 32];
+      return u;
+    } else {
+      return load8_at<HF32, QUADS>(base, el + r * 256, in0[r], in1[r]);
+    }
+  };
+  const auto d_at = [&](const uint4* src, int word, const void* base, int64_t el, int r) {
+    if constexpr (RING) {
+      Raw<DF32> u;
+#pragma unroll
+      for (int j = 0; j < DW; ++j) u.w[j] = src[(word + r * DW + j) * 32];
+      return u;
+    } else {
+      return load8_at<DF32, QUADS>(base, el + r * 256, in0[r], in1[r]);
+    }
+  };
+  if constexpr (RING)  // words that no copy fills (past the row's end) stay zero
+    for (int i = 0; i < p.depth * p.words; ++i) mine[i * 32] = make_uint4(0, 0, 0, 0);
+  float* const s_w = reinterpret_cast<float*>(s_ring + (blockDim.x >> 5) * p.depth * p.words * 32);
+  if constexpr (R <= 2)
+    if (p.w != nullptr) {
+      for (int i = threadIdx.x; i < p.warps * R * 32; i += blockDim.x) {
+        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (i < p.nvec) {
+          if (p.w_f32)
+            load8<true>(p.w, i, f);
+          else
+            load8<false>(p.w, i, f);
+        }
+        *reinterpret_cast<float4*>(s_w + 8 * i) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(s_w + 8 * i + 4) = make_float4(f[4], f[5], f[6], f[7]);
+      }
+    }
+
+  f32x2 acc[R][4];
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[r][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) acc[r][e] = pair(0.0f, 0.0f);
+  if constexpr (RING) {
+    int64_t row = first;
+    for (int d = 0; d < p.depth; ++d, row += stride) {
+      if (row < p.t) fetch(row, mine + d * slot_step);
+      copy_commit();
+    }
+  }
+  if constexpr (R <= 2) __syncthreads();  // the weight
 
-  int parity = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kGroups + group; row < p.t; row += int64_t(gridDim.x) * kGroups) {
-    const int64_t base = row * p.nvec;
-    const float rstd = p.rstd[row];
-    float n[R][8], g[R][8];
+  int slot = 0, parity = 0;
+  float rstd_next = first < p.t ? p.rstd[first] : 0.0f;
+  for (int64_t row = first; row < p.t; row += stride) {
+    const int64_t el = row * k + at;
+    const float rstd = rstd_next;
+    if (row + stride < p.t) rstd_next = p.rstd[row + stride];
+    if constexpr (RING) {
+      if (p.depth == 3)
+        copy_wait<2>();
+      else if (p.depth == 2)
+        copy_wait<1>();
+      else
+        copy_wait<0>();
+    }
+    uint4* const src = mine + slot * slot_step;
+    const f32x2 rstd2 = pair(rstd, rstd);
+    f32x2 n[R][4], g[R][4], c2 = pair(0.0f, 0.0f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = r * TPR + tid;
+      f32x2 u[4];
+      h_at(src, 0, p.h, el, r).unpack(n[r]);
+      d_at(src, kDy, p.dy[0], el, r).unpack(g[r]);
+      if (p.ndy > 1) {
+        d_at(src, kDy + kOne, p.dy[1], el, r).unpack(u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) n[r][e] = g[r][e] = 0.0f;
-      if (i < p.nvec) {
-        load8<HF32>(p.h, base + i, n[r]);
-        load8<DF32>(p.dy[0], base + i, g[r]);
-        float q[8];
-        if (p.ndy > 1) {
-          load8<DF32>(p.dy[1], base + i, q);
+        for (int e = 0; e < 4; ++e) g[r][e] = add2(g[r][e], u[e]);
+      }
+      if (p.ndy > 2) {
+        d_at(src, kDy + 2 * kOne, p.dy[2], el, r).unpack(u);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[r][e] += q[e];
+        for (int e = 0; e < 4; ++e) g[r][e] = add2(g[r][e], u[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        n[r][e] = mul2(n[r][e], rstd2);
+        acc[r][e] = fma2(g[r][e], n[r][e], acc[r][e]);
+      }
+      if (p.w != nullptr) {
+        if constexpr (R <= 2) {
+          const float4* w = reinterpret_cast<const float4*>(s_w + at + r * 256);
+          const float4 a = w[0], b = w[QUADS ? 32 : 1];
+          u[0] = pair(a.x, a.y), u[1] = pair(a.z, a.w), u[2] = pair(b.x, b.y), u[3] = pair(b.z, b.w);
+        } else if (p.w_f32) {
+          load8_at<true, QUADS>(p.w, at + r * 256, in0[r], in1[r]).unpack(u);
+        } else {
+          load8_at<false, QUADS>(p.w, at + r * 256, in0[r], in1[r]).unpack(u);
         }
-        if (p.ndy > 2) {
-          load8<DF32>(p.dy[2], base + i, q);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[r][e] += q[e];
-        }
+        for (int e = 0; e < 4; ++e) g[r][e] = mul2(g[r][e], u[e]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c2 = fma2(g[r][e], n[r][e], c2);
     }
-    float c = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = r * TPR + tid;
-      float w[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-      if (p.w != nullptr && i < p.nvec) {
-        if (p.w_f32)
-          load8<true>(p.w, i, w);
-        else
-          load8<false>(p.w, i, w);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        n[r][e] *= rstd;
-        acc[r][e] = fmaf(g[r][e], n[r][e], acc[r][e]);
-        g[r][e] *= w[e];
-        c = fmaf(g[r][e], n[r][e], c);
-      }
-    }
+    const float2 ch = halves(c2);
+    float c = ch.x + ch.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    if constexpr (TPR > 32) {
-      if (lane == 0) s_part[parity][group][warp] = c;
-      group_sync<TPR>(group);
-      c = 0.0f;
+    if (p.warps > 1) {
+      if (lane == 0) s_part[parity][warp] = c;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.warps * 32) : "memory");
+      c = (lane & 15) < p.warps ? s_part[parity][group * p.warps + (lane & 15)] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) c += s_part[parity][group][i];
-      parity ^= 1;  // a slot is written again two rows on, behind another barrier
+      for (int o = 8; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      parity ^= 1;  // a place is written again two rows on, behind another barrier
     }
-    c *= p.inv_k;
+    c *= -p.inv_k;
+    const f32x2 minus = pair(c, c);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = r * TPR + tid;
-      if (i >= p.nvec) continue;
-      float d[8];
+      f32x2 d[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = rstd * fmaf(-n[r][e], c, g[r][e]);
+      for (int e = 0; e < 4; ++e) d[e] = mul2(rstd2, fma2(n[r][e], minus, g[r][e]));
       if (p.dres != nullptr) {
-        float q[8];
-        load8<HF32>(p.dres, base + i, q);
+        f32x2 u[4];
+        h_at(src, kRes, p.dres, el, r).unpack(u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] += q[e];
+        for (int e = 0; e < 4; ++e) d[e] = add2(d[e], u[e]);
       }
-      store8<HF32>(p.dh, base + i, d);
-      if (p.dx != nullptr) p.dx[base + i] = pack8(d);
+      const uint4 b = pack8(d);
+      if constexpr (HF32) {
+        const float2 d0 = halves(d[0]), d1 = halves(d[1]), d2 = halves(d[2]), d3 = halves(d[3]);
+        float* dst = static_cast<float*>(p.dh) + el + r * 256;
+        if (in0[r]) *reinterpret_cast<float4*>(dst) = make_float4(d0.x, d0.y, d1.x, d1.y);
+        if (in1[r]) *reinterpret_cast<float4*>(dst + 128) = make_float4(d2.x, d2.y, d3.x, d3.y);
+      } else {
+        store8_bf16<QUADS>(p.dh, el + r * 256, b, in0[r], in1[r]);
+      }
+      if (p.dx != nullptr) store8_bf16<QUADS>(p.dx, el + r * 256, b, in0[r], in1[r]);
+    }
+    if constexpr (RING) {  // this row's slot is read: the copies of a row to come may take it
+      const int64_t later = row + p.depth * stride;
+      if (later < p.t) fetch(later, src);
+      copy_commit();
+      if (++slot == p.depth) slot = 0;
     }
   }
   if (p.part == nullptr) return;
-  float4* dst = reinterpret_cast<float4*>(p.part) + int64_t(blockIdx.x) * (2 * p.nvec);
-  if constexpr (kGroups == 1) {
+  float* dst = p.part + int64_t(blockIdx.x) * k;
+  float* sum = reinterpret_cast<float*>(s_ring);
+  copy_wait<0>();
+  if (p.groups > 1) __syncthreads();  // every group is done with the ring
+  for (int gr = 0; gr < p.groups; ++gr) {  // the groups' shares, one group after the other
+    if (p.groups > 1) __syncthreads();
+    if (group != gr) continue;
+    float* to = gr == p.groups - 1 ? dst : sum;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = r * TPR + tid;
-      if (i >= p.nvec) continue;
-      dst[2 * i] = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
-      dst[2 * i + 1] = make_float4(acc[r][4], acc[r][5], acc[r][6], acc[r][7]);
-    }
-  } else {  // the groups' shares, one group after the other
-    for (int gr = 0; gr < kGroups; ++gr) {
-      if (group == gr) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float4* s = s_dw + 2 * (r * TPR + tid);
-          float4 a = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
-          float4 b = make_float4(acc[r][4], acc[r][5], acc[r][6], acc[r][7]);
-          if (gr > 0) {
-            a.x += s[0].x, a.y += s[0].y, a.z += s[0].z, a.w += s[0].w;
-            b.x += s[1].x, b.y += s[1].y, b.z += s[1].z, b.w += s[1].w;
-          }
-          s[0] = a, s[1] = b;
+      for (int q = 0; q < 2; ++q) {
+        const int i = at + r * 256 + q * (QUADS ? 128 : 4);
+        if (!(q ? in1[r] : in0[r])) continue;
+        const float2 a0 = halves(acc[r][2 * q]), a1 = halves(acc[r][2 * q + 1]);
+        float4 a = make_float4(a0.x, a0.y, a1.x, a1.y);
+        if (gr > 0) {
+          const float4 u = *reinterpret_cast<const float4*>(sum + i);
+          a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
         }
+        *reinterpret_cast<float4*>(to + i) = a;
       }
-      __syncthreads();
-    }
-    for (int i = threadIdx.x; i < 2 * p.nvec; i += kBlock) dst[i] = s_dw[i];
   }
 }
 
@@ -620,31 +763,49 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float4* __restrict__ part
   if (y == 0 && col < n4) dw[col] = a;
 }
 
-template <bool HF32, bool DF32, int TPR, int R>
-cudaError_t launch_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t s) {
-  constexpr int block = kNormBwdBlock(TPR), groups = block / TPR;
-  const int64_t want = (p.t + groups - 1) / groups;
-  const int blocks = static_cast<int>(want < num_sms ? want : num_sms);
-  const cudaError_t e =
-      launch_pdl(k_rmsnorm_bwd<HF32, DF32, TPR, R>, dim3(blocks), dim3(block), 0, s, p);
+template <bool HF32, bool DF32, int R, bool RING>
+cudaError_t launch_norm_bwd(const NormBwdParams& p, int blocks, size_t smem, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd<HF32, DF32, R, RING>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_rmsnorm_bwd<HF32, DF32, R, RING>, dim3(blocks), dim3(32 * p.warps * p.groups), smem, s, p);
+}
+
+// Two runs a warp (one where a warp holds the row, four where 20 warps do not),
+// and of the numbers of rows that a block can work on at a time the one with the
+// most rows in its ring, but no more than there are rows for all SMs; one block
+// an SM.
+template <bool HF32, bool DF32>
+cudaError_t pick_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t s) {
+  const int r = p.nvec <= 32 ? 1 : p.nvec <= 1024 ? 2 : 4;
+  const int most_warps = (r <= 2 ? kNormBwdThreads : 512) / 32;
+  p.warps = (p.nvec + 32 * r - 1) / (32 * r);
+  p.words = r * ((HF32 ? 2 : 1) * 2 + (DF32 ? 2 : 1) * p.ndy);
+  const size_t weight = r <= 2 && p.w != nullptr ? size_t(p.warps) * r * 1024 : 0;  // fp32, behind the ring
+  const size_t room = 224 * 1024 - weight;
+  const size_t one = size_t(p.words) * 16 * 32 * p.warps;
+  const auto depth = [&](int groups) { return static_cast<int>(std::min<size_t>(room / (one * groups), 3)); };
+  const int most = static_cast<int>(std::min<int64_t>({most_warps / p.warps, 15, (p.t + num_sms - 1) / num_sms}));
+  p.groups = most;
+  for (int g = most - 1; g >= 1; --g)
+    if (g * depth(g) > p.groups * depth(p.groups)) p.groups = g;
+  p.depth = depth(p.groups);
+  const size_t row = one * p.groups;
+  const size_t smem = std::max<size_t>(p.depth * row + weight, p.groups > 1 ? size_t(p.nvec) * 32 : 0);
+  const int blocks = static_cast<int>(std::min<int64_t>(p.t, num_sms));
+  cudaError_t e;
+  if (r == 1)
+    e = launch_norm_bwd<HF32, DF32, 1, true>(p, blocks, smem, s);
+  else if (r == 2)
+    e = launch_norm_bwd<HF32, DF32, 2, true>(p, blocks, smem, s);  // a row takes 163,840 bytes at most
+  else if (p.depth > 0)
+    e = launch_norm_bwd<HF32, DF32, 4, true>(p, blocks, smem, s);
+  else
+    e = launch_norm_bwd<HF32, DF32, 4, false>(p, blocks, smem, s);
   if (e != cudaSuccess || dw == nullptr) return e;
   const int n4 = 2 * p.nvec;
   return launch_pdl(k_norm_dw, dim3((n4 + 7) / 8), dim3(256), 0, s, reinterpret_cast<const float4*>(p.part), blocks,
                     n4, reinterpret_cast<float4*>(dw));
-}
-
-template <bool HF32, bool DF32>
-cudaError_t pick_norm_bwd(const NormBwdParams& p, float* dw, int num_sms, cudaStream_t s) {
-  const int n = p.nvec;
-  if (n <= 32) return launch_norm_bwd<HF32, DF32, 32, 1>(p, dw, num_sms, s);
-  if (n <= 64) return launch_norm_bwd<HF32, DF32, 32, 2>(p, dw, num_sms, s);
-  if (n <= 128) return launch_norm_bwd<HF32, DF32, 32, 4>(p, dw, num_sms, s);
-  if (n <= 256) return launch_norm_bwd<HF32, DF32, 128, 2>(p, dw, num_sms, s);
-  if (n <= 384) return launch_norm_bwd<HF32, DF32, 128, 3>(p, dw, num_sms, s);
-  if (n <= 512) return launch_norm_bwd<HF32, DF32, 128, 4>(p, dw, num_sms, s);
-  if (n <= 1024) return launch_norm_bwd<HF32, DF32, 512, 2>(p, dw, num_sms, s);
-  if (n <= 1536) return launch_norm_bwd<HF32, DF32, 512, 3>(p, dw, num_sms, s);
-  return launch_norm_bwd<HF32, DF32, 512, 4>(p, dw, num_sms, s);
 }
 
 }  // namespace
@@ -674,7 +835,7 @@ cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s
   p.t = a.t, p.nvec = static_cast<int>(a.k / 8);
   p.inv_k = 1.0f / static_cast<float>(a.k);
   p.w_f32 = (a.flags & SBL_NORM_W_F32) != 0u;
-  p.dh = a.dh, p.dx = static_cast<uint4*>(a.dx);
+  p.dh = a.dh, p.dx = a.dx;
   p.part = a.dw != nullptr ? static_cast<float*>(a.workspace) : nullptr;
   if (num_sms > kNormBwdMaxBlocks) num_sms = kNormBwdMaxBlocks;
   const bool hf = (a.flags & SBL_NORM_STREAM_F32) != 0u, df = (a.flags & SBL_NORM_DY_F32) != 0u;
