@@ -464,8 +464,9 @@ sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* ta
  * row's loss, dloss[i * dloss_stride] (stride 0: one value for all rows).
  *   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]), 0 for ignored rows and rows with a bad target
  *   dh = dz w  bf16 [t, d],   dw = dz^T h  bf16 [v, d]
- * The logits are computed again, a piece of the vocabulary at a time; dz is
- * rounded to bf16 for the two products, which accumulate in fp32.
+ * The logits are computed again, a piece of the vocabulary at a time.  For the
+ * two products, which accumulate in fp32, exp(z - lse) - [j = target] is
+ * rounded to bf16, and for dw also dloss_i h_i (not with stride 0).
  * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 1) bytes, 256-byte
  * aligned.  t == 0: dw = 0. */
 sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,

@@ -11,12 +11,18 @@
 // the epilogue warps under the next tile's product.
 //
 // Backward, a piece of the vocabulary at a time, so that dz (bf16, at most
-// kCeDzBytes) stays in L2 between its writer and its two readers: one launch
-// computes the piece's logits again and writes dz, a second one runs both
-// products over it.  dw rows belong to one piece; dh adds up over the pieces
+// kCeDzBytes) stays in L2 between its writer and its two readers: a launch
+// computes a piece's logits again and writes dz, and runs both products over
+// the piece before.  dw rows belong to one piece; dh adds up over the pieces
 // in fp32.  With few tokens dh has few output tiles and a long sum over the
 // vocabulary, which is then split over slices that a last launch joins.
 #include <algorithm>
+#include <array>
+#include <functional>
+#include <map>
+#include <queue>
+#include <utility>
+#include <vector>
 
 #include "gemm_launch.cuh"
 
@@ -96,19 +102,16 @@ struct CfgCeFwd : CfgCeLogits<CeFwdParams> {
       tmem_load_32x32b_x32(t_acc + c * 32, r);
       tmem_load_wait();
       const int left = p.v - col0;
-      float z[32], best = top;
+      const int64_t at = target - col0;
+      const bool mine = in && at >= 0 && at < 32 && target < p.v;  // the target's logit is in this chunk
+      float z[32], best = top, hit = 0.0f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         z[e] = e < left ? __uint_as_float(r[e]) : -INFINITY;
         best = fmaxf(best, z[e]);
+        if (mine && e == int(at)) hit += z[e];
       }
-      const int64_t at = target - col0;
-      if (at >= 0 && at < 32 && in) {
-        float hit = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) hit = e == int(at) ? z[e] : hit;
-        if (target < p.v) p.hit[row] = hit;
-      }
+      if (mine) p.hit[row] = hit;
       const float base = best == -INFINITY ? 0.0f : best;
       sum *= exp_of(top - base);
 #pragma unroll
@@ -161,43 +164,160 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Backward: dz of one piece of the vocabulary
+// Backward.  One launch works on three kinds of tiles at once, none of which
+// needs another's result of the same launch:
+//   dz   of the next piece (into the other of two buffers):
+//        A = h [t][d], B = the piece's rows of w, both K-major, K = d
+//   dh   of this piece:  A = dz [t][v] K-major, B = w's rows MN-major, K = v,
+//        in `slices` runs of k_run blocks of 64
+//   dw   of this piece:  A = dz MN-major (M = v), B = the scaled h MN-major, K = t
+// so that a piece costs one launch and the short tiles fill the gaps that the
+// deep ones leave.  Every operand is read in boxes of 64 x 64, which both
+// majors can use, so one tensor map each serves h, w and dz.
+//
+// dz holds exp(z - lse) - [j = target] without the row's gradient dloss: its
+// largest entries are then next to -1, where bf16 is exact for small
+// probabilities, and a row's factor stays out of that rounding.  dh multiplies
+// its fp32 sums by dloss, dw takes h already multiplied by it (one rounding to
+// bf16; one value for all rows multiplies the fp32 sums instead).
 // ---------------------------------------------------------------------------
-struct CeDzParams {
-  int t, v, d;  // v: entries of this piece
-  int64_t first;
-  int64_t ld;   // elements of a dz row
-  uint16_t* dz;
+constexpr int kCeMaxPairs = 96;
+constexpr int kCeMaxTiles = 4096;
+constexpr int kCeTileCost = 4;  // of a tile beside its blocks, in blocks: filling the pipe, the last epilogue
+
+struct CeBwdParams {
+  int t, d;
+  int zv, vv;           // entries of the next piece (dz) and of this one (dh, dw); 0: none
+  int64_t zfirst, vfirst;
+  int64_t ld;           // elements of a dz row
+  uint16_t* dz;         // the next piece's dz
   const int64_t* targets;
   int64_t v_all, ignore;
   const float* lse;
   const float* dloss;
   int64_t dloss_stride;
+  int slices, k_run;
+  float* acc;           // [slices][t][d] fp32 sums of dh, or nullptr: dh is written directly
+  int add;              // acc holds the earlier pieces' sum
+  int last;             // with one slice: write dh instead of acc
+  uint16_t *dh, *dw;    // dw: this piece's rows
   uint32_t* status;
+  int tabled;           // tiles from the table, else striped
+  uint16_t sched_off[kCeMaxPairs + 1];
+  uint16_t sched[kCeMaxTiles];
 };
 
-struct CfgCeDz : CfgCeLogits<CeDzParams> {
-  using Tiles = StripedTiles<CfgCeDz>;
+struct CfgCeBwd {
+  using Params = CeBwdParams;
+  static constexpr bool QUANT_X = false;
+  static constexpr int MAPS = 4;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
+  static constexpr int A_BYTES = 128 * BK * 2;
+  static constexpr int B_BYTES = (BN / 2) * BK * 2;
+  static constexpr int E_BYTES = 0;
+  static constexpr int ACC_COLS = BN;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int E_COL0 = 0, E_COLS = 0;
+  enum { kDz = 0, kDw = 1, kDh = 2 };  // a tile's problem; kDh + slice for dh
 
-  __device__ static void epilogue(const CeDzParams& p, int, uint32_t t_acc, int row, int n0, int, int part,
+  __host__ __device__ static int up(int a, int b) { return (a + b - 1) / b; }
+  __host__ __device__ static int tiles_dz(const Params& p) { return up(p.t, 256) * up(p.zv, 256); }
+  __host__ __device__ static int tiles_dh(const Params& p) { return p.vv ? up(p.t, 256) * up(p.d, 256) * p.slices : 0; }
+  __host__ __device__ static int tiles_dw(const Params& p) { return up(p.vv, 256) * up(p.d, 256); }
+
+  struct Tiles {
+    __device__ static int count(const Params& p, int pair, int npairs) {
+      if (p.tabled) return p.sched_off[pair + 1] - p.sched_off[pair];
+      const int n = tiles_dz(p) + tiles_dh(p) + tiles_dw(p);
+      return pair < n ? (n - pair + npairs - 1) / npairs : 0;
+    }
+    // Tile numbers: dh, then dw, then dz; the blocks of the same operand rows next to each other.
+    __device__ static PairTile at(const Params& p, int pair, int npairs, int i) {
+      int id = p.tabled ? p.sched[p.sched_off[pair] + i] : pair + i * npairs;
+      const int mt = up(p.t, 256), nd = up(p.d, 256), mv = up(p.vv, 256);
+      if (id < tiles_dh(p)) {
+        const int slice = id / (mt * nd);
+        id -= slice * mt * nd;
+        return PairTile{kDh + slice, id % mt, id / mt, min(up(p.vv, BK) - slice * p.k_run, p.k_run)};
+      }
+      id -= tiles_dh(p);
+      if (id < tiles_dw(p)) return PairTile{kDw, id % mv, id / mv, up(p.t, BK)};
+      id -= tiles_dw(p);
+      return PairTile{kDz, id % mt, id / mt, up(p.d, BK)};
+    }
+  };
+
+  // Maps: h, w, this piece's dz, h times dloss.
+  __device__ static void load_stage(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tz,
+                                    const CUtensorMap* ths, const Params& p, int prob, uint8_t* sA, uint8_t* sB,
+                                    uint8_t*, int m0, int n0, int kb, uint64_t* bar) {
+    int k0 = kb * BK;
+    if (prob == kDz) {
+      const int w0 = int(p.zfirst) + n0;
+      tma_load_2d_pair(sA, th, k0, m0, bar);  // [64 m][64 k] x 2
+      tma_load_2d_pair(sA + 8192, th, k0, m0 + 64, bar);
+      tma_load_2d_pair(sB, tw, k0, w0, bar);
+      tma_load_2d_pair(sB + 8192, tw, k0, w0 + 64, bar);
+    } else if (prob == kDw) {
+      tma_load_2d_pair(sA, tz, m0, k0, bar);  // [64 k][64 m] x 2
+      tma_load_2d_pair(sA + 8192, tz, m0 + 64, k0, bar);
+      tma_load_2d_pair(sB, ths, n0, k0, bar);
+      tma_load_2d_pair(sB + 8192, ths, n0 + 64, k0, bar);
+    } else {
+      k0 += (prob - kDh) * p.k_run * BK;
+      const int w0 = int(p.vfirst) + k0;
+      tma_load_2d_pair(sA, tz, k0, m0, bar);  // [64 m][64 k] x 2
+      tma_load_2d_pair(sA + 8192, tz, k0, m0 + 64, bar);
+      tma_load_2d_pair(sB, tw, n0, w0, bar);  // [64 k][64 n] x 2
+      tma_load_2d_pair(sB + 8192, tw, n0 + 64, w0, bar);
+    }
+  }
+
+  __device__ static void mma_stage(const Params&, int prob, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB,
+                                   uint8_t*, bool first) {
+    const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+    const bool a_mn = prob == kDw, b_mn = prob != kDz;
+    const uint32_t idesc = prob == kDz ? idesc_bf16(256, BN, false, false)
+                           : prob == kDw ? idesc_bf16(256, BN, true, true) : idesc_bf16(256, BN, false, true);
+#pragma unroll
+    for (int kk = 0; kk < BK / 16; ++kk) {
+      const uint64_t ad = a_mn ? smem_desc(a0 + kk * 2048, 8192, 1024, 2) : smem_desc(a0 + kk * 32, 16, 1024, 2);
+      const uint64_t bd = b_mn ? smem_desc(b0 + kk * 2048, 8192, 1024, 2) : smem_desc(b0 + kk * 32, 16, 1024, 2);
+      mma_bf16_pair(d_tmem, ad, bd, idesc, (first && kk == 0) ? 0u : 1u);
+    }
+  }
+
+  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row, int n0, int, int part,
                                   int parts) {
+    if (prob == kDz)
+      epilogue_dz(p, t_acc, row, n0, part, parts);
+    else
+      epilogue_product(p, prob, t_acc, row, n0, part, parts);
+  }
+
+  __device__ static __forceinline__ bool good(const Params& p, int64_t target) {
+    return target >= 0 && target < p.v_all && target != p.ignore;
+  }
+
+  __device__ static __forceinline__ void epilogue_dz(const Params& p, uint32_t t_acc, int row, int n0, int part,
+                                                     int parts) {
     const bool in = row < p.t;
-    const int64_t target = in ? __ldcg(p.targets + row) : -1;
-    const bool good = target >= 0 && target < p.v_all && target != p.ignore;
-    if (in && !good && target != p.ignore && n0 == 0 && p.first == 0 && part == 0)
+    const int64_t target = in ? __ldcg(p.targets + row) : p.ignore;
+    const bool live = in && good(p, target);
+    if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0 && part == 0)
       raise_status(p.status, SBL_STATUS_BAD_TARGET);
-    const float lse = in ? __ldcg(p.lse + row) : 0.0f;
-    const float scale = good ? __ldcg(p.dloss + row * p.dloss_stride) : 0.0f;
+    const float lse = live ? __ldcg(p.lse + row) : 0.0f;
 #pragma unroll 1
     for (int c = part; c < BN / 32; c += parts) {
       const int col0 = n0 + c * 32;
-      if (col0 >= p.v) break;  // uniform across the warp
+      if (col0 >= p.zv) break;  // uniform across the warp
       uint32_t r[32];
       __syncwarp();
       tmem_load_32x32b_x32(t_acc + c * 32, r);
       tmem_load_wait();
       if (!in) continue;  // after the warp-wide load
-      const int64_t at = target - p.first - col0;
+      const int64_t at = target - p.zfirst - col0;
       uint4* dst = reinterpret_cast<uint4*>(p.dz + int64_t(row) * p.ld + col0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -208,112 +328,28 @@ struct CfgCeDz : CfgCeLogits<CeDzParams> {
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             const int j = 8 * q + 2 * e + f;
-            float x = exp_of(__uint_as_float(r[j]) - lse);
-            if (at == j) x -= 1.0f;
-            y[f] = scale != 0.0f ? x * scale : 0.0f;
+            y[f] = exp_of(__uint_as_float(r[j]) - lse);
+            if (at == j) y[f] -= 1.0f;
+            if (!live) y[f] = 0.0f;
           }
           const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[0], y[1]);
           packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
         }
-        if (col0 + 8 * q < p.v) dst[q] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        if (col0 + 8 * q < p.zv) dst[q] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
       }
     }
   }
-};
 
-// ---------------------------------------------------------------------------
-// Backward: both products over a piece's dz in one launch.
-//   problem 0 (dh):  A = dz [t][v] K-major, B = w piece [v][d] MN-major, K = v
-//                    in `slices` runs of k_run blocks of 64
-//   problem 1 (dw):  A = dz MN-major (M = v), B = h [t][d] MN-major, K = t
-// Tiles of the deeper problem first, striped over the pairs.  A tile's problem
-// number carries its slice: 2 * slice for dh, 1 for dw.
-// ---------------------------------------------------------------------------
-struct CeProductParams {
-  int t, v, d;
-  int slices, k_run;  // dh: runs of the sum over v
-  int mb0, mb1, nb;   // 256-wide blocks of t, v and d
-  int dh_first;
-  float* acc;         // [slices][t][d] fp32, or nullptr: dh is written directly
-  int add;            // acc holds the earlier pieces' sum
-  int last;           // with one slice: write dh instead of acc
-  uint16_t *dh, *dw;  // dw: this piece's rows
-  uint32_t* status;
-};
-
-struct CfgCeProducts {
-  using Params = CeProductParams;
-  static constexpr bool QUANT_X = false;
-  static constexpr int MAPS = 4;
-  static constexpr int EPI_WARPS = 4;
-  static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
-  static constexpr int A_BYTES = 128 * BK * 2;
-  static constexpr int B_BYTES = (BN / 2) * BK * 2;
-  static constexpr int E_BYTES = 0;
-  static constexpr int ACC_COLS = BN;
-  static constexpr int TMEM_COLS = 512;
-  static constexpr int E_COL0 = 0, E_COLS = 0;
-  static constexpr uint32_t IDESC0 = idesc_bf16(256, BN, false, true);
-  static constexpr uint32_t IDESC1 = idesc_bf16(256, BN, true, true);
-
-  __host__ __device__ static int tiles0(const Params& p) { return p.mb0 * p.nb * p.slices; }
-  __host__ __device__ static int tiles1(const Params& p) { return p.mb1 * p.nb; }
-
-  struct Tiles {
-    __device__ static int count(const Params& p, int pair, int npairs) {
-      const int n = tiles0(p) + tiles1(p);
-      return pair < n ? (n - pair + npairs - 1) / npairs : 0;
-    }
-    __device__ static PairTile at(const Params& p, int pair, int npairs, int i) {
-      int id = pair + i * npairs;
-      const int first = p.dh_first ? tiles0(p) : tiles1(p);
-      const bool dh = (id < first) == (p.dh_first != 0);
-      if (id >= first) id -= first;
-      if (!dh) return PairTile{1, id % p.mb1, id / p.mb1, (p.t + BK - 1) / BK};
-      const int slice = id / (p.mb0 * p.nb);
-      id -= slice * p.mb0 * p.nb;
-      const int blocks = (p.v + BK - 1) / BK - slice * p.k_run;
-      return PairTile{2 * slice, id % p.mb0, id / p.mb0, min(blocks, p.k_run)};
-    }
-  };
-
-  // Maps: dz (K-major boxes), w, dz (MN-major boxes), h.
-  __device__ static void load_stage(const CUtensorMap* tA, const CUtensorMap* tB, const CUtensorMap* tA1,
-                                    const CUtensorMap* tB1, const Params& p, int prob, uint8_t* sA, uint8_t* sB,
-                                    uint8_t*, int m0, int n0, int kb, uint64_t* bar) {
-    if (prob != 1) {
-      const int k0 = ((prob >> 1) * p.k_run + kb) * BK;
-      tma_load_2d_pair(sA, tA, k0, m0, bar);  // [128 m][64 k]
-      tma_load_2d_pair(sB, tB, n0, k0, bar);  // [64 k][64 n] x 2
-      tma_load_2d_pair(sB + 8192, tB, n0 + 64, k0, bar);
-    } else {
-      const int k0 = kb * BK;
-      tma_load_2d_pair(sA, tA1, m0, k0, bar);  // [64 k][64 m] x 2
-      tma_load_2d_pair(sA + 8192, tA1, m0 + 64, k0, bar);
-      tma_load_2d_pair(sB, tB1, n0, k0, bar);
-      tma_load_2d_pair(sB + 8192, tB1, n0 + 64, k0, bar);
-    }
-  }
-
-  __device__ static void mma_stage(const Params&, int prob, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB,
-                                   uint8_t*, bool first) {
-    const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
-    const bool dw = prob == 1;
-#pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      const uint64_t ad = dw ? smem_desc(a0 + kk * 2048, 8192, 1024, 2) : smem_desc(a0 + kk * 32, 16, 1024, 2);
-      const uint64_t bd = smem_desc(b0 + kk * 2048, 8192, 1024, 2);
-      mma_bf16_pair(d_tmem, ad, bd, dw ? IDESC1 : IDESC0, (first && kk == 0) ? 0u : 1u);
-    }
-  }
-
-  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row, int n0, int, int part,
-                                  int parts) {
-    const bool dw = prob == 1;
+  __device__ static __forceinline__ void epilogue_product(const Params& p, int prob, uint32_t t_acc, int row, int n0,
+                                                          int part, int parts) {
+    const bool dw = prob == kDw;
     const bool to_acc = !dw && p.acc != nullptr && !p.last;
     const bool add = !dw && p.acc != nullptr && p.add;
-    const int rows = dw ? p.v : p.t;
-    float* acc = to_acc || add ? p.acc + (int64_t(prob >> 1) * p.t + row) * p.d : nullptr;
+    const bool in = row < (dw ? p.vv : p.t);
+    float scale = 1.0f;
+    if (in && dw && p.dloss_stride == 0) scale = __ldcg(p.dloss);
+    if (in && !dw && !to_acc) scale = good(p, __ldcg(p.targets + row)) ? __ldcg(p.dloss + row * p.dloss_stride) : 0.0f;
+    float* acc = to_acc || add ? p.acc + (int64_t(prob - kDh) * p.t + row) * p.d : nullptr;
     uint16_t* out = (dw ? p.dw : p.dh) + int64_t(row) * p.d;
 #pragma unroll 1
     for (int c = part; c < BN / 32; c += parts) {
@@ -322,7 +358,7 @@ struct CfgCeProducts {
       tmem_load_32x32b_x32(t_acc + c * 32, r);
       tmem_load_wait();
       const int col0 = n0 + c * 32;
-      if (row >= rows || col0 >= p.d) continue;  // after the warp-wide load
+      if (!in || col0 >= p.d) continue;  // after the warp-wide load
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int col = col0 + 8 * q;
@@ -343,7 +379,7 @@ struct CfgCeProducts {
           uint32_t packed[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[2 * e] * scale, f[2 * e + 1] * scale);
             packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           *reinterpret_cast<uint4*>(out + col) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
@@ -353,19 +389,45 @@ struct CfgCeProducts {
   }
 };
 
-// dh = the sum of its slices, in their order.
+// h times each row's dloss, zero for rows without loss: 8 elements a thread.
 __global__ void __launch_bounds__(256)
-    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t n4, uint2* __restrict__ dh) {
+    k_ce_scale(const uint4* __restrict__ h, const int64_t* __restrict__ targets, const float* __restrict__ dloss,
+               int64_t vecs, int row_vecs, int64_t v, int64_t ignore, uint4* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= vecs) return;
+  const int64_t row = i / row_vecs, target = targets[row];
+  const bool live = target >= 0 && target < v && target != ignore;
+  const float g = live ? dloss[row] : 0.0f;
+  const uint4 x = h[i];
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 h2 =
+        __floats2bfloat162_rn(__uint_as_float(in[e] << 16) * g, __uint_as_float(in[e] & 0xFFFF0000u) * g);
+    o[e] = live ? *reinterpret_cast<const uint32_t*>(&h2) : 0u;
+  }
+  out[i] = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// dh = dloss times the sum of its slices, in their order: 4 elements a thread.
+__global__ void __launch_bounds__(256)
+    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t n4, int row_n4, const int64_t* __restrict__ targets,
+            const float* __restrict__ dloss, int64_t dloss_stride, int64_t v, int64_t ignore, uint2* __restrict__ dh) {
   pdl_wait();
   pdl_trigger();
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
+  const int64_t row = i / row_n4, target = targets[row];
+  const float g = target >= 0 && target < v && target != ignore ? dloss[row * dloss_stride] : 0.0f;
   float4 a = __ldcg(acc + i);
   for (int s = 1; s < slices; ++s) {
     const float4 b = __ldcg(acc + s * n4 + i);
     a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
   }
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * g, a.y * g), hi = __floats2bfloat162_rn(a.z * g, a.w * g);
   dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
@@ -376,7 +438,8 @@ struct CePlan {
   int64_t piece;    // vocabulary entries of a piece, a multiple of 256
   int64_t pieces;
   int slices, k_run;
-  uint64_t dz_bytes, acc_bytes;
+  uint64_t dz_bytes, acc_bytes, scaled_bytes;  // dz: one buffer of two (one piece: of one)
+  uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + scaled_bytes; }
 };
 
 CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
@@ -387,8 +450,9 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   c.piece = ((padded / 256 + c.pieces - 1) / c.pieces) * 256;  // even pieces
   c.pieces = (padded + c.piece - 1) / c.piece;
   c.dz_bytes = align_up(uint64_t(t) * uint64_t(c.piece) * 2, 256);
-  // dh in one piece's launch: its tiles are as deep as the piece is wide.  A
-  // run of the sum is at most what each pair has to do anyway (or 8 blocks).
+  c.scaled_bytes = align_up(uint64_t(t) * uint64_t(d) * 2, 256);
+  // A dh tile is as deep as the piece is wide.  A run of the sum is at most
+  // what each pair of SMs has to do anyway (or 8 blocks).
   const int64_t nb = (d + 255) / 256, mb0 = (t + 255) / 256, mb1 = c.piece / 256;
   const int64_t kb0 = (std::min(c.piece, v) + 63) / 64, kb1 = (t + 63) / 64, pairs = 74;  // 148 SMs
   const int64_t share = std::max<int64_t>((mb0 * nb * kb0 + mb1 * nb * kb1) / pairs, 8);
@@ -399,6 +463,44 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   return c;
 }
 
+// The tiles of one launch over the pairs, deepest first, each to the pair with
+// the least work so far.  Cached per shape.
+struct CeSchedule {
+  std::vector<uint16_t> off, ids;
+};
+
+const CeSchedule& ce_schedule(int n_dh, int k_dh, int n_dw, int k_dw, int n_dz, int k_dz, int npairs) {
+  static std::mutex mu;
+  static std::map<std::array<int, 7>, CeSchedule> cache;
+  std::lock_guard<std::mutex> lock(mu);
+  const std::array<int, 7> key = {n_dh, k_dh, n_dw, k_dw, n_dz, k_dz, npairs};
+  const auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  struct Kind {
+    int first, n, depth;
+  };
+  Kind kinds[3] = {{0, n_dh, k_dh}, {n_dh, n_dw, k_dw}, {n_dh + n_dw, n_dz, k_dz}};
+  std::stable_sort(kinds, kinds + 3, [](const Kind& a, const Kind& b) { return a.depth > b.depth; });
+  std::vector<std::vector<uint16_t>> per(npairs);
+  using Load = std::pair<int64_t, int>;  // work so far, pair
+  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> least;
+  for (int q = 0; q < npairs; ++q) least.push({0, q});
+  for (const Kind& k : kinds)
+    for (int i = 0; i < k.n; ++i) {
+      const Load l = least.top();
+      least.pop();
+      per[l.second].push_back(static_cast<uint16_t>(k.first + i));
+      least.push({l.first + k.depth + kCeTileCost, l.second});
+    }
+  CeSchedule sch;
+  sch.off.push_back(0);
+  for (const auto& ids : per) {
+    sch.ids.insert(sch.ids.end(), ids.begin(), ids.end());
+    sch.off.push_back(static_cast<uint16_t>(sch.ids.size()));
+  }
+  return cache.emplace(key, std::move(sch)).first->second;
+}
+
 bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   return encode_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, ld * 2, 64, box_rows,
                         CU_TENSOR_MAP_SWIZZLE_128B);
@@ -407,10 +509,7 @@ bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows
 }  // namespace
 
 uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
-  if (backward) {
-    const CePlan c = ce_plan(t, v, d);
-    return c.dz_bytes + c.acc_bytes;
-  }
+  if (backward) return ce_plan(t, v, d).total();
   const uint64_t pieces = 2 * ((uint64_t(v) + kCeTile - 1) / kCeTile);
   return align_up(uint64_t(t) * pieces * 8, 256) + align_up(uint64_t(t) * 4, 256);
 }
@@ -433,49 +532,64 @@ cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   const CePlan c = ce_plan(a.t, a.v, a.d);
-  uint16_t* dz = static_cast<uint16_t*>(a.workspace);
-  float* acc = c.acc_bytes ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + c.dz_bytes) : nullptr;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  uint16_t* dz[2] = {reinterpret_cast<uint16_t*>(ws), reinterpret_cast<uint16_t*>(ws + (c.pieces > 1 ? c.dz_bytes : 0))};
+  ws += c.dz_bytes * (c.pieces > 1 ? 2 : 1);
+  float* acc = c.acc_bytes ? reinterpret_cast<float*>(ws) : nullptr;
+  ws += c.acc_bytes;
+  const uint16_t* scaled = a.h;
+  cudaError_t e;
+  if (a.dloss_stride != 0) {
+    const int64_t vecs = a.t * a.d / 8;
+    e = launch_pdl(k_ce_scale, dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0, s,
+                   reinterpret_cast<const uint4*>(a.h), a.targets, a.dloss, vecs, static_cast<int>(a.d / 8), a.v,
+                   a.ignore_index, reinterpret_cast<uint4*>(ws));
+    if (e != cudaSuccess) return e;
+    scaled = reinterpret_cast<const uint16_t*>(ws);
+  }
   int max_clusters = 0;
-  cudaError_t e = pair_setup<CfgCeProducts>(num_sms, &max_clusters);
-  if (e != cudaSuccess) return e;
-  CUtensorMap th, th_mn;
-  if (!rows_map(&th, a.h, a.d, a.t, a.d, 128) || !rows_map(&th_mn, a.h, a.d, a.t, a.d, 64))
+  if ((e = pair_setup<CfgCeBwd>(num_sms, &max_clusters)) != cudaSuccess) return e;
+  CUtensorMap th, tw, ths;
+  if (!rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
+      !rows_map(&ths, scaled, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
-  for (int64_t i = 0; i < c.pieces; ++i) {
-    const int64_t first = i * c.piece, wide = std::min(c.piece, a.v - first);
-    const uint16_t* w = a.w + first * a.d;
-    CUtensorMap tw, tw_mn, tz, tz_mn;
-    if (!rows_map(&tw, w, a.d, wide, a.d, 128) || !rows_map(&tw_mn, w, a.d, wide, a.d, 64) ||
-        !rows_map(&tz, dz, wide, a.t, c.piece, 128) || !rows_map(&tz_mn, dz, wide, a.t, c.piece, 64))
-      return cudaErrorInvalidValue;
-    CeDzParams z;
-    z.t = static_cast<int>(a.t), z.v = static_cast<int>(wide), z.d = static_cast<int>(a.d);
-    z.first = first, z.ld = c.piece, z.dz = dz;
-    z.targets = a.targets, z.v_all = a.v, z.ignore = a.ignore_index;
-    z.lse = a.lse, z.dloss = a.dloss, z.dloss_stride = a.dloss_stride;
-    z.status = a.status;
-    if ((e = launch_pair<CfgCeDz>(th, tw, tw, z, z.t, z.v, num_sms, s, true)) != cudaSuccess) return e;
-    CeProductParams p;
-    p.t = z.t, p.v = z.v, p.d = z.d;
+  const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
+  for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
+    CeBwdParams p;
+    p.t = static_cast<int>(a.t), p.d = static_cast<int>(a.d);
+    p.zv = static_cast<int>(wide(i + 1)), p.zfirst = (i + 1) * c.piece;
+    p.vv = static_cast<int>(wide(i)), p.vfirst = i * c.piece;
+    p.ld = c.piece, p.dz = dz[(i + 1) & 1];
+    p.targets = a.targets, p.v_all = a.v, p.ignore = a.ignore_index;
+    p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride;
     p.k_run = c.k_run;
-    p.slices = static_cast<int>(((wide + 63) / 64 + c.k_run - 1) / c.k_run);
-    p.mb0 = (p.t + 255) / 256, p.mb1 = (p.v + 255) / 256, p.nb = (p.d + 255) / 256;
-    p.dh_first = std::min<int64_t>(c.k_run, (wide + 63) / 64) >= (p.t + 63) / 64;
+    p.slices = ((p.vv + 63) / 64 + c.k_run - 1) / c.k_run;
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
-    p.dh = a.dh, p.dw = a.dw + first * a.d;
+    p.dh = a.dh, p.dw = a.dw + std::max<int64_t>(p.vfirst, 0) * a.d;
     p.status = a.status;
-    const int64_t tiles = int64_t(CfgCeProducts::tiles0(p)) + CfgCeProducts::tiles1(p);
-    const int pairs = static_cast<int>(std::min<int64_t>(tiles, max_clusters));
-    e = launch_pdl(k_gemm_pair<CfgCeProducts>, dim3(2 * pairs), dim3(pair_threads<CfgCeProducts>()),
-                   pair_smem_bytes<CfgCeProducts>(), s, tz, tw_mn, tz_mn, th_mn, p);
+    CUtensorMap tz = th;
+    if (p.vv > 0 && !rows_map(&tz, dz[i & 1], p.vv, a.t, c.piece, 64)) return cudaErrorInvalidValue;
+    const int n_dh = CfgCeBwd::tiles_dh(p), n_dw = CfgCeBwd::tiles_dw(p), n_dz = CfgCeBwd::tiles_dz(p);
+    const int64_t tiles = int64_t(n_dh) + n_dw + n_dz;
+    const int pairs = static_cast<int>(std::min<int64_t>({tiles, max_clusters, kCeMaxPairs}));
+    p.tabled = tiles <= kCeMaxTiles;
+    if (p.tabled) {
+      const CeSchedule& sch = ce_schedule(n_dh, std::min(c.k_run, (p.vv + 63) / 64), n_dw, (p.t + 63) / 64, n_dz,
+                                          (p.d + 63) / 64, pairs);
+      std::copy(sch.off.begin(), sch.off.end(), p.sched_off);
+      std::copy(sch.ids.begin(), sch.ids.end(), p.sched);
+    }
+    e = launch_pdl(k_gemm_pair<CfgCeBwd>, dim3(2 * pairs), dim3(pair_threads<CfgCeBwd>()), pair_smem_bytes<CfgCeBwd>(),
+                   s, th, tw, tz, ths, p);
     if (e != cudaSuccess) return e;
   }
   if (c.slices > 1) {
     const int64_t n4 = a.t * a.d / 4;
     return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
-                      reinterpret_cast<const float4*>(acc), c.slices, n4, reinterpret_cast<uint2*>(a.dh));
+                      reinterpret_cast<const float4*>(acc), c.slices, n4, static_cast<int>(a.d / 4), a.targets, a.dloss,
+                      a.dloss_stride, a.v, a.ignore_index, reinterpret_cast<uint2*>(a.dh));
   }
   return cudaSuccess;
 }

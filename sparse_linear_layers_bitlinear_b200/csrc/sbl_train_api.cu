@@ -200,7 +200,11 @@ sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* t
   a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dloss_stride = dloss_stride;
   a.dh = static_cast<uint16_t*>(dh), a.dw = static_cast<uint16_t*>(dw);
   a.workspace = workspace, a.status = status_dev;
-  return code(launch_linear_ce_bwd(a, sms, s));
+  try {
+    return code(launch_linear_ce_bwd(a, sms, s));
+  } catch (const std::bad_alloc&) {
+    return SBL_ERR_CUDA;  // no host memory for the tile schedule
+  }
 }
 
 }  // extern "C"
