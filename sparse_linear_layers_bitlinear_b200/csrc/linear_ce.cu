@@ -42,7 +42,7 @@ struct CfgCeLogits {
   using Params = P;
   static constexpr bool QUANT_X = false;
   static constexpr int MAPS = 2;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARPS = 4, PARTS = EPI_WARPS / 4;
   static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
   static constexpr int A_BYTES = 128 * BK * 2;       // 16 KB
   static constexpr int B_BYTES = (BN / 2) * BK * 2;  // 16 KB
@@ -118,7 +118,7 @@ struct CfgCeFwd : CfgCeLogits<CeFwdParams> {
       for (int e = 0; e < 32; ++e) sum += exp_of(z[e] - base);
       top = best;
     }
-    if (in) p.piece[int64_t(row) * p.pieces + 2 * (n0 / BN) + part] = make_float2(top, sum);
+    if (in) p.piece[int64_t(row) * p.pieces + PARTS * (n0 / BN) + part] = make_float2(top, sum);
   }
 };
 
@@ -211,7 +211,7 @@ struct CfgCeBwd {
   using Params = CeBwdParams;
   static constexpr bool QUANT_X = false;
   static constexpr int MAPS = 4;
-  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_WARPS = 4;
   static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = (BN / 2) * BK * 2;
@@ -510,7 +510,7 @@ bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows
 
 uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
   if (backward) return ce_plan(t, v, d).total();
-  const uint64_t pieces = 2 * ((uint64_t(v) + kCeTile - 1) / kCeTile);
+  const uint64_t pieces = CfgCeFwd::PARTS * ((uint64_t(v) + kCeTile - 1) / kCeTile);
   return align_up(uint64_t(t) * pieces * 8, 256) + align_up(uint64_t(t) * 4, 256);
 }
 
@@ -519,7 +519,7 @@ cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
   if (!rows_map(&th, a.h, a.d, a.t, a.d, 128) || !rows_map(&tw, a.w, a.d, a.v, a.d, 128)) return cudaErrorInvalidValue;
   CeFwdParams p;
   p.t = static_cast<int>(a.t), p.v = static_cast<int>(a.v), p.d = static_cast<int>(a.d);
-  p.pieces = 2 * ((p.v + kCeTile - 1) / kCeTile);
+  p.pieces = CfgCeFwd::PARTS * ((p.v + kCeTile - 1) / kCeTile);
   p.piece = static_cast<float2*>(a.workspace);
   p.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + align_up(uint64_t(a.t) * p.pieces * 8, 256));
   p.targets = a.targets;
