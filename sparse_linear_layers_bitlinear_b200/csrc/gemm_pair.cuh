@@ -55,6 +55,17 @@ struct PairSmemTail {
   int abort_flag;
 };
 
+// Shared memory that a configuration's epilogue stages its output tiles in
+// (OUT_BYTES a CTA; 0 for those that store from registers).
+template <class Cfg, class = void>
+struct PairOut {
+  static constexpr int bytes = 0;
+};
+template <class Cfg>
+struct PairOut<Cfg, decltype(void(Cfg::OUT_BYTES))> {
+  static constexpr int bytes = Cfg::OUT_BYTES;
+};
+
 template <class Cfg>
 constexpr int pair_threads() {
   return 64 + 32 * Cfg::EPI_WARPS;
@@ -64,13 +75,14 @@ template <class Cfg>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(), 1)
     k_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmF,
-                const typename Cfg::Params p) {
+                const __grid_constant__ typename Cfg::Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* smA = smem;
   uint8_t* smB = smA + Cfg::STAGES * Cfg::A_BYTES;
   uint8_t* smE = smB + Cfg::STAGES * Cfg::B_BYTES;
-  PairSmemTail* tail = reinterpret_cast<PairSmemTail*>(smE + Cfg::STAGES * Cfg::E_BYTES);
+  uint8_t* smO = smE + Cfg::STAGES * Cfg::E_BYTES;
+  PairSmemTail* tail = reinterpret_cast<PairSmemTail*>(smO + PairOut<Cfg>::bytes);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -227,10 +239,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
       const int m0 = t.mb * 256 + 128 * int(rank);
       const int n0 = t.nb * Cfg::BN;
       const uint32_t t_acc = tmem_base + ab * Cfg::ACC_COLS + (uint32_t(quarter * 32) << 16);
-      Cfg::epilogue(p, t.prob, t_acc, m0 + quarter * 32 + lane, n0, lane, part, parts);
+      if constexpr (PairOut<Cfg>::bytes > 0)
+        Cfg::epilogue(p, t.prob, t_acc, m0 + quarter * 32, n0, lane,
+                      smO + (warp - 2) * (PairOut<Cfg>::bytes / Cfg::EPI_WARPS));
+      else
+        Cfg::epilogue(p, t.prob, t_acc, m0 + quarter * 32 + lane, n0, lane, part, parts);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(leader_acc_empty0 + ab * 8u);
+    }
+    if constexpr (PairOut<Cfg>::bytes > 0) {
+      if (lane == 0) bulk_store_wait_all();  // before the CTA gives its shared memory back
     }
   }
 
@@ -246,7 +265,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
 
 template <class Cfg>
 constexpr int pair_smem_bytes() {
-  return 1024 + Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES + Cfg::E_BYTES) + int(sizeof(PairSmemTail));
+  return 1024 + Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES + Cfg::E_BYTES) + PairOut<Cfg>::bytes +
+         int(sizeof(PairSmemTail));
 }
 
 // ---------------------------------------------------------------------------

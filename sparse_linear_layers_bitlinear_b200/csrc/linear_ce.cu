@@ -186,21 +186,19 @@ constexpr int kCeMaxTiles = 4096;
 constexpr int kCeTileCost = 4;  // of a tile beside its blocks, in blocks: filling the pipe, the last epilogue
 
 struct CeBwdParams {
+  CUtensorMap dz_out, dw_out, dh_out, acc_out;  // of the stores: bf16 boxes of 64 x 32 rows, acc: fp32, 32 x 32
   int t, d;
   int zv, vv;           // entries of the next piece (dz) and of this one (dh, dw); 0: none
   int64_t zfirst, vfirst;
-  int64_t ld;           // elements of a dz row
-  uint16_t* dz;         // the next piece's dz
   const int64_t* targets;
   int64_t v_all, ignore;
   const float* lse;
   const float* dloss;
   int64_t dloss_stride;
   int slices, k_run;
-  float* acc;           // [slices][t][d] fp32 sums of dh, or nullptr: dh is written directly
+  const float* acc;     // [slices][t up to a multiple of 32][d] fp32 sums of dh, or nullptr: dh is written directly
   int add;              // acc holds the earlier pieces' sum
   int last;             // with one slice: write dh instead of acc
-  uint16_t *dh, *dw;    // dw: this piece's rows
   uint32_t* status;
   int tabled;           // tiles from the table, else striped
   uint16_t sched_off[kCeMaxPairs + 1];
@@ -216,6 +214,7 @@ struct CfgCeBwd {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = (BN / 2) * BK * 2;
   static constexpr int E_BYTES = 0;
+  static constexpr int OUT_BYTES = EPI_WARPS * 2 * 4096;  // two boxes of 32 rows x 128 bytes a warp
   static constexpr int ACC_COLS = BN;
   static constexpr int TMEM_COLS = 512;
   static constexpr int E_COL0 = 0, E_COLS = 0;
@@ -288,103 +287,113 @@ struct CfgCeBwd {
     }
   }
 
-  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row, int n0, int, int part,
-                                  int parts) {
-    if (prob == kDz)
-      epilogue_dz(p, t_acc, row, n0, part, parts);
-    else
-      epilogue_product(p, prob, t_acc, row, n0, part, parts);
-  }
-
   __device__ static __forceinline__ bool good(const Params& p, int64_t target) {
     return target >= 0 && target < p.v_all && target != p.ignore;
   }
 
-  __device__ static __forceinline__ void epilogue_dz(const Params& p, uint32_t t_acc, int row, int n0, int part,
-                                                     int parts) {
-    const bool in = row < p.t;
-    const int64_t target = in ? __ldcg(p.targets + row) : p.ignore;
-    const bool live = in && good(p, target);
-    if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0 && part == 0)
-      raise_status(p.status, SBL_STATUS_BAD_TARGET);
-    const float lse = live ? __ldcg(p.lse + row) : 0.0f;
-#pragma unroll 1
-    for (int c = part; c < BN / 32; c += parts) {
-      const int col0 = n0 + c * 32;
-      if (col0 >= p.zv) break;  // uniform across the warp
-      uint32_t r[32];
-      __syncwarp();
-      tmem_load_32x32b_x32(t_acc + c * 32, r);
-      tmem_load_wait();
-      if (!in) continue;  // after the warp-wide load
-      const int64_t at = target - p.zfirst - col0;
-      uint4* dst = reinterpret_cast<uint4*>(p.dz + int64_t(row) * p.ld + col0);
+  // A lane's row of a box (32 words, 128 bytes) goes to shared memory in the
+  // 128-byte swizzle, the warp's 32 rows to global memory by one TMA store:
+  // whole lines instead of 16 bytes a row (which cost the dz launch a seventh
+  // of its time).  Two boxes in turn, from the first one at every tile; the box
+  // before the last has been read when this one is filled.
+  __device__ static __forceinline__ void put(const CUtensorMap* map, const uint32_t (&word)[32], uint8_t* box, int lane,
+                                             int x, int y, bool add) {
+    if (lane == 0) bulk_store_wait_read<1>();
+    __syncwarp();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t packed[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y[2];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int j = 8 * q + 2 * e + f;
-            y[f] = exp_of(__uint_as_float(r[j]) - lse);
-            if (at == j) y[f] -= 1.0f;
-            if (!live) y[f] = 0.0f;
-          }
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(y[0], y[1]);
-          packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-        if (col0 + 8 * q < p.zv) dst[q] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-      }
+    for (int c = 0; c < 8; ++c)
+      *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+          make_uint4(word[4 * c], word[4 * c + 1], word[4 * c + 2], word[4 * c + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (add)
+        tma_add_2d(map, box, x, y);
+      else
+        tma_store_2d(map, box, x, y);
+      bulk_store_commit();
     }
   }
 
-  __device__ static __forceinline__ void epilogue_product(const Params& p, int prob, uint32_t t_acc, int row, int n0,
-                                                          int part, int parts) {
-    const bool dw = prob == kDw;
-    const bool to_acc = !dw && p.acc != nullptr && !p.last;
-    const bool add = !dw && p.acc != nullptr && p.add;
-    const bool in = row < (dw ? p.vv : p.t);
-    float scale = 1.0f;
-    if (in && dw && p.dloss_stride == 0) scale = __ldcg(p.dloss);
-    if (in && !dw && !to_acc) scale = good(p, __ldcg(p.targets + row)) ? __ldcg(p.dloss + row * p.dloss_stride) : 0.0f;
-    float* acc = to_acc || add ? p.acc + (int64_t(prob - kDh) * p.t + row) * p.d : nullptr;
-    uint16_t* out = (dw ? p.dw : p.dh) + int64_t(row) * p.d;
+  // row0: the warp's first row, one row a lane.
+  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row0, int n0, int lane, uint8_t* box) {
+    const bool dz = prob == kDz, dw = prob == kDw;
+    const int rows = dw ? p.vv : p.t, cols = dz ? p.zv : p.d;
+    if (row0 >= rows) return;
+    if (lane == 0) bulk_store_wait_read<0>();  // the tile before
+    const int row = row0 + lane;
+    const bool in = row < rows;
+    if (!dz && !dw && p.acc != nullptr && !p.last) {  // dh's fp32 sums: stored by the first piece, then added to
+      const int y = (prob - kDh) * up(p.t, 32) * 32 + row0;
 #pragma unroll 1
-    for (int c = part; c < BN / 32; c += parts) {
-      uint32_t r[32];
-      __syncwarp();
-      tmem_load_32x32b_x32(t_acc + c * 32, r);
-      tmem_load_wait();
-      const int col0 = n0 + c * 32;
-      if (!in || col0 >= p.d) continue;  // after the warp-wide load
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_load_32x32b_x32(t_acc + c * 32, r);
+        tmem_load_wait();
+        if (n0 + c * 32 >= cols) break;
+        put(&p.acc_out, r, box + (c & 1) * 4096, lane, n0 + c * 32, y, p.add);
+      }
+      return;
+    }
+    const int64_t target = !dw && in ? __ldcg(p.targets + row) : p.ignore;
+    const bool live = good(p, target);
+    float factor = 0.0f, lse = 0.0f;
+    if (dz) {
+      if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0) raise_status(p.status, SBL_STATUS_BAD_TARGET);
+      if (live) lse = __ldcg(p.lse + row);
+    } else if (dw) {
+      factor = p.dloss_stride == 0 ? __ldcg(p.dloss) : 1.0f;
+    } else if (live) {
+      factor = __ldcg(p.dloss + row * p.dloss_stride);
+    }
+    const CUtensorMap* map = dz ? &p.dz_out : dw ? &p.dw_out : &p.dh_out;
+#pragma unroll 1
+    for (int c = 0; c < BN / 64; ++c) {
+      const int col0 = n0 + c * 64;
+      if (col0 >= cols) break;  // uniform across the warp
+      uint32_t word[32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = col0 + 8 * q;
-        if (col >= p.d) break;  // d is a multiple of 8
-        float f[8];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_load_32x32b_x32(t_acc + c * 64 + h * 32, r);
+        tmem_load_wait();
+        if (dz) {
+          const int64_t at = target - p.zfirst - col0 - h * 32;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(r[8 * q + e]);
-        if (add) {  // through L2: another SM may have written it in the launch before
-          const float4 a = __ldcg(reinterpret_cast<const float4*>(acc + col));
-          const float4 b = __ldcg(reinterpret_cast<const float4*>(acc + col) + 1);
-          f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
-          f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
-        }
-        if (to_acc) {
-          reinterpret_cast<float4*>(acc + col)[0] = make_float4(f[0], f[1], f[2], f[3]);
-          reinterpret_cast<float4*>(acc + col)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-          uint32_t packed[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(f[2 * e] * scale, f[2 * e + 1] * scale);
-            packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+          for (int e = 0; e < 32; ++e) {
+            float x = exp_of(__uint_as_float(r[e]) - lse);
+            if (at == e) x -= 1.0f;
+            r[e] = __float_as_uint(live ? x : 0.0f);
           }
-          *reinterpret_cast<uint4*>(out + col) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        } else {
+          if (!dw && p.add && in) {  // dh's last piece.  Through L2: another SM wrote it in the launch before
+            const float* acc = p.acc + int64_t(row) * p.d + col0 + h * 32;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (col0 + h * 32 + 4 * q >= p.d) break;
+              const float4 a = __ldcg(reinterpret_cast<const float4*>(acc) + q);
+              r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + a.x);
+              r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + a.y);
+              r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + a.z);
+              r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + a.w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
+          if (!dw && !live) {  // whatever the sums of a row without loss are (zero, but for NaN operands)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+          word[16 * h + e] = *reinterpret_cast<const uint32_t*>(&h2);
         }
       }
+      put(map, word, box + (c & 1) * 4096, lane, col0, row0, false);
     }
   }
 };
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(256)
 
 // dh = dloss times the sum of its slices, in their order: 4 elements a thread.
 __global__ void __launch_bounds__(256)
-    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t n4, int row_n4, const int64_t* __restrict__ targets,
+    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t slice_n4, int64_t n4, int row_n4, const int64_t* __restrict__ targets,
             const float* __restrict__ dloss, int64_t dloss_stride, int64_t v, int64_t ignore, uint2* __restrict__ dh) {
   pdl_wait();
   pdl_trigger();
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(256)
   const float g = target >= 0 && target < v && target != ignore ? dloss[row * dloss_stride] : 0.0f;
   float4 a = __ldcg(acc + i);
   for (int s = 1; s < slices; ++s) {
-    const float4 b = __ldcg(acc + s * n4 + i);
+    const float4 b = __ldcg(acc + s * slice_n4 + i);
     a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * g, a.y * g), hi = __floats2bfloat162_rn(a.z * g, a.w * g);
@@ -459,7 +468,7 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   int64_t slices = std::min<int64_t>((kb0 + share - 1) / share, 32);
   c.k_run = static_cast<int>((kb0 + slices - 1) / slices);
   c.slices = static_cast<int>((kb0 + c.k_run - 1) / c.k_run);
-  c.acc_bytes = (c.pieces > 1 || c.slices > 1) ? align_up(uint64_t(c.slices) * uint64_t(t) * uint64_t(d) * 4, 256) : 0;
+  c.acc_bytes = (c.pieces > 1 || c.slices > 1) ? align_up(uint64_t(c.slices) * align_up(t, 32) * uint64_t(d) * 4, 256) : 0;
   return c;
 }
 
@@ -549,8 +558,11 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   }
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd>(num_sms, &max_clusters)) != cudaSuccess) return e;
-  CUtensorMap th, tw, ths;
-  if (!rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
+  CUtensorMap th, tw, ths, dh_out, acc_out;
+  if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * ((a.t + 31) / 32 * 32), a.d * 4, 32,
+                                        32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (!rows_map(&dh_out, a.dh, a.d, a.t, a.d, 32) || !rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
       !rows_map(&ths, scaled, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
@@ -559,7 +571,6 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     p.t = static_cast<int>(a.t), p.d = static_cast<int>(a.d);
     p.zv = static_cast<int>(wide(i + 1)), p.zfirst = (i + 1) * c.piece;
     p.vv = static_cast<int>(wide(i)), p.vfirst = i * c.piece;
-    p.ld = c.piece, p.dz = dz[(i + 1) & 1];
     p.targets = a.targets, p.v_all = a.v, p.ignore = a.ignore_index;
     p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride;
     p.k_run = c.k_run;
@@ -567,10 +578,14 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
-    p.dh = a.dh, p.dw = a.dw + std::max<int64_t>(p.vfirst, 0) * a.d;
     p.status = a.status;
     CUtensorMap tz = th;
-    if (p.vv > 0 && !rows_map(&tz, dz[i & 1], p.vv, a.t, c.piece, 64)) return cudaErrorInvalidValue;
+    p.dz_out = p.dw_out = p.acc_out = p.dh_out = dh_out;
+    if (p.zv > 0 && !rows_map(&p.dz_out, dz[(i + 1) & 1], p.zv, a.t, c.piece, 32)) return cudaErrorInvalidValue;
+    if (p.vv > 0 && (!rows_map(&tz, dz[i & 1], p.vv, a.t, c.piece, 64) ||
+                     !rows_map(&p.dw_out, a.dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
+      return cudaErrorInvalidValue;
+    if (acc != nullptr) p.acc_out = acc_out;
     const int n_dh = CfgCeBwd::tiles_dh(p), n_dw = CfgCeBwd::tiles_dw(p), n_dz = CfgCeBwd::tiles_dz(p);
     const int64_t tiles = int64_t(n_dh) + n_dw + n_dz;
     const int pairs = static_cast<int>(std::min<int64_t>({tiles, max_clusters, kCeMaxPairs}));
@@ -588,7 +603,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   if (c.slices > 1) {
     const int64_t n4 = a.t * a.d / 4;
     return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
-                      reinterpret_cast<const float4*>(acc), c.slices, n4, static_cast<int>(a.d / 4), a.targets, a.dloss,
+                      reinterpret_cast<const float4*>(acc), c.slices, (a.t + 31) / 32 * 32 * a.d / 4, n4, static_cast<int>(a.d / 4), a.targets, a.dloss,
                       a.dloss_stride, a.v, a.ignore_index, reinterpret_cast<uint2*>(a.dh));
   }
   return cudaSuccess;
