@@ -66,6 +66,21 @@ struct PairOut<Cfg, decltype(void(Cfg::OUT_BYTES))> {
   static constexpr int bytes = Cfg::OUT_BYTES;
 };
 
+// Configurations whose tiles are of MMA_KINDS kinds have the loop over a tile's
+// stages compiled for each.
+template <int KIND>
+struct PairKind {
+  static constexpr int value = KIND;
+};
+template <class Cfg, class = void>
+struct PairKinds {
+  static constexpr int count = 1;
+};
+template <class Cfg>
+struct PairKinds<Cfg, decltype(void(Cfg::MMA_KINDS))> {
+  static constexpr int count = Cfg::MMA_KINDS;
+};
+
 template <class Cfg>
 constexpr int pair_threads() {
   return 64 + 32 * Cfg::EPI_WARPS;
@@ -174,19 +189,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + ab * Cfg::ACC_COLS;
-        for (int kb = 0; kb < t.kblocks; ++kb) {
-          if (!mbar_wait(&tail->full[stage], phase, abort_flag, status)) {
-            ok = false;
-            break;
+        // The tile's stages; `issue` puts one stage's MMAs into the pipe.
+        const auto stages = [&](auto issue) {
+          for (int kb = 0; kb < t.kblocks; ++kb) {
+            if (!mbar_wait(&tail->full[stage], phase, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            issue(kb == 0);
+            mma_commit_pair(&tail->empty[stage]);  // frees the stage in both CTAs once these MMAs have read it
+            if (++stage == Cfg::STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          tc_fence_after();
-          Cfg::mma_stage(p, t.prob, d_tmem, tmem_base + Cfg::E_COL0 + (stage & 1u) * Cfg::E_COLS,
-                         smA + stage * Cfg::A_BYTES, smB + stage * Cfg::B_BYTES, smE + stage * Cfg::E_BYTES, kb == 0);
-          mma_commit_pair(&tail->empty[stage]);  // frees the stage in both CTAs once these MMAs have read it
-          if (++stage == Cfg::STAGES) {
-            stage = 0;
-            phase ^= 1u;
+        };
+        if constexpr (PairKinds<Cfg>::count == 3) {
+          const auto of_kind = [&](auto kind) {
+            stages([&](bool first) {
+              Cfg::template mma_stage<decltype(kind)::value>(d_tmem, smA + stage * Cfg::A_BYTES,
+                                                             smB + stage * Cfg::B_BYTES, first);
+            });
+          };
+          switch (Cfg::mma_kind(t.prob)) {
+            case 0: of_kind(PairKind<0>{}); break;
+            case 1: of_kind(PairKind<1>{}); break;
+            default: of_kind(PairKind<2>{}); break;
           }
+        } else {
+          stages([&](bool first) {
+            Cfg::mma_stage(p, t.prob, d_tmem, tmem_base + Cfg::E_COL0 + (stage & 1u) * Cfg::E_COLS,
+                           smA + stage * Cfg::A_BYTES, smB + stage * Cfg::B_BYTES, smE + stage * Cfg::E_BYTES, first);
+          });
         }
         if (!ok) break;
         mma_commit_pair(&tail->acc_full[ab]);  // accumulator complete in both CTAs
@@ -222,6 +257,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
         if (lane == 0) atomicAdd(p.ready + row / Cfg::BN, 1u);
       }
     }
+    if constexpr (PairOut<Cfg>::bytes > 0)  // work for the warps whose first accumulator is still to come
+      Cfg::prologue(p, int(blockIdx.x) * Cfg::EPI_WARPS + (warp - 2), int(gridDim.x) * Cfg::EPI_WARPS, lane);
     for (int i = 0; i < ntiles; ++i) {
       const PairTile t = Cfg::Tiles::at(p, pair, npairs, i);
       const uint32_t ab = uint32_t(i) & 1u;

@@ -59,8 +59,10 @@ struct CfgCeLogits {
   __device__ static void load_stage(const CUtensorMap* tA, const CUtensorMap* tB, const CUtensorMap*,
                                     const CUtensorMap*, const P&, int, uint8_t* sA, uint8_t* sB, uint8_t*, int m0,
                                     int n0, int kb, uint64_t* bar) {
-    tma_load_2d_pair(sA, tA, kb * BK, m0, bar);
+    tma_load_2d_pair(sA, tA, kb * BK, m0, bar);  // [64 rows][64 k] x 2
+    tma_load_2d_pair(sA + 8192, tA, kb * BK, m0 + 64, bar);
     tma_load_2d_pair(sB, tB, kb * BK, n0, bar);
+    tma_load_2d_pair(sB + 8192, tB, kb * BK, n0 + 64, bar);
   }
 
   __device__ static void mma_stage(const P&, int, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB, uint8_t*,
@@ -199,6 +201,8 @@ struct CeBwdParams {
   const float* acc;     // [slices][t up to a multiple of 32][d] fp32 sums of dh, or nullptr: dh is written directly
   int add;              // acc holds the earlier pieces' sum
   int last;             // with one slice: write dh instead of acc
+  const uint16_t* h;
+  uint16_t* scaled;     // the first launch: where h times dloss goes (or nullptr)
   uint32_t* status;
   int tabled;           // tiles from the table, else striped
   uint16_t sched_off[kCeMaxPairs + 1];
@@ -217,7 +221,6 @@ struct CfgCeBwd {
   static constexpr int OUT_BYTES = EPI_WARPS * 2 * 4096;  // two boxes of 32 rows x 128 bytes a warp
   static constexpr int ACC_COLS = BN;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int E_COL0 = 0, E_COLS = 0;
   enum { kDz = 0, kDw = 1, kDh = 2 };  // a tile's problem; kDh + slice for dh
 
   __host__ __device__ static int up(int a, int b) { return (a + b - 1) / b; }
@@ -273,22 +276,52 @@ struct CfgCeBwd {
     }
   }
 
-  __device__ static void mma_stage(const Params&, int prob, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB,
-                                   uint8_t*, bool first) {
+  // One thread issues every MMA of a pair, so a stage's issue has to stay far
+  // below the 512 cycles its MMAs take: the loop over a tile's stages is
+  // compiled once for each kind, with constant descriptors.
+  static constexpr int MMA_KINDS = 3;
+  __device__ static int mma_kind(int prob) { return min(prob, int(kDh)); }
+  template <int KIND>
+  __device__ static void mma_stage(uint32_t d_tmem, uint8_t* sA, uint8_t* sB, bool first) {
+    constexpr bool a_mn = KIND == kDw, b_mn = KIND != kDz;
     const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
-    const bool a_mn = prob == kDw, b_mn = prob != kDz;
-    const uint32_t idesc = prob == kDz ? idesc_bf16(256, BN, false, false)
-                           : prob == kDw ? idesc_bf16(256, BN, true, true) : idesc_bf16(256, BN, false, true);
 #pragma unroll
     for (int kk = 0; kk < BK / 16; ++kk) {
       const uint64_t ad = a_mn ? smem_desc(a0 + kk * 2048, 8192, 1024, 2) : smem_desc(a0 + kk * 32, 16, 1024, 2);
       const uint64_t bd = b_mn ? smem_desc(b0 + kk * 2048, 8192, 1024, 2) : smem_desc(b0 + kk * 32, 16, 1024, 2);
-      mma_bf16_pair(d_tmem, ad, bd, idesc, (first && kk == 0) ? 0u : 1u);
+      mma_bf16_pair(d_tmem, ad, bd, idesc_bf16(256, BN, a_mn, b_mn), (first && kk == 0) ? 0u : 1u);
     }
   }
 
   __device__ static __forceinline__ bool good(const Params& p, int64_t target) {
     return target >= 0 && target < p.v_all && target != p.ignore;
+  }
+
+  // The first launch: h times each row's dloss for dw, zero for rows without
+  // loss, a row a warp, while the first tiles' products run.
+  __device__ static void prologue(const Params& p, int warp, int warps, int lane) {
+    if (p.scaled == nullptr) return;
+    pdl_wait();  // h, targets and dloss may come from the kernel before
+    const int vecs = p.d / 8;
+    for (int row = warp; row < p.t; row += warps) {
+      const bool live = good(p, __ldcg(p.targets + row));
+      const float g = live ? __ldcg(p.dloss + row) : 0.0f;
+      const uint4* src = reinterpret_cast<const uint4*>(p.h) + int64_t(row) * vecs;
+      uint4* dst = reinterpret_cast<uint4*>(p.scaled) + int64_t(row) * vecs;
+#pragma unroll 4
+      for (int i = lane; i < vecs; i += 32) {
+        const uint4 x = __ldcg(src + i);
+        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 h2 =
+              __floats2bfloat162_rn(__uint_as_float(in[e] << 16) * g, __uint_as_float(in[e] & 0xFFFF0000u) * g);
+          o[e] = live ? *reinterpret_cast<const uint32_t*>(&h2) : 0u;
+        }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
   }
 
   // A lane's row of a box (32 words, 128 bytes) goes to shared memory in the
@@ -398,29 +431,6 @@ struct CfgCeBwd {
   }
 };
 
-// h times each row's dloss, zero for rows without loss: 8 elements a thread.
-__global__ void __launch_bounds__(256)
-    k_ce_scale(const uint4* __restrict__ h, const int64_t* __restrict__ targets, const float* __restrict__ dloss,
-               int64_t vecs, int row_vecs, int64_t v, int64_t ignore, uint4* __restrict__ out) {
-  pdl_wait();
-  pdl_trigger();
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= vecs) return;
-  const int64_t row = i / row_vecs, target = targets[row];
-  const bool live = target >= 0 && target < v && target != ignore;
-  const float g = live ? dloss[row] : 0.0f;
-  const uint4 x = h[i];
-  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-  uint32_t o[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 h2 =
-        __floats2bfloat162_rn(__uint_as_float(in[e] << 16) * g, __uint_as_float(in[e] & 0xFFFF0000u) * g);
-    o[e] = live ? *reinterpret_cast<const uint32_t*>(&h2) : 0u;
-  }
-  out[i] = make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // dh = dloss times the sum of its slices, in their order: 4 elements a thread.
 __global__ void __launch_bounds__(256)
     k_ce_dh(const float4* __restrict__ acc, int slices, int64_t slice_n4, int64_t n4, int row_n4, const int64_t* __restrict__ targets,
@@ -525,7 +535,7 @@ uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
 
 cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
   CUtensorMap th, tw;
-  if (!rows_map(&th, a.h, a.d, a.t, a.d, 128) || !rows_map(&tw, a.w, a.d, a.v, a.d, 128)) return cudaErrorInvalidValue;
+  if (!rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64)) return cudaErrorInvalidValue;
   CeFwdParams p;
   p.t = static_cast<int>(a.t), p.v = static_cast<int>(a.v), p.d = static_cast<int>(a.d);
   p.pieces = CfgCeFwd::PARTS * ((p.v + kCeTile - 1) / kCeTile);
@@ -546,16 +556,9 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   ws += c.dz_bytes * (c.pieces > 1 ? 2 : 1);
   float* acc = c.acc_bytes ? reinterpret_cast<float*>(ws) : nullptr;
   ws += c.acc_bytes;
-  const uint16_t* scaled = a.h;
+  // dw's operand: h times dloss, or h itself where one dloss multiplies the sums
+  uint16_t* scaled = a.dloss_stride != 0 ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   cudaError_t e;
-  if (a.dloss_stride != 0) {
-    const int64_t vecs = a.t * a.d / 8;
-    e = launch_pdl(k_ce_scale, dim3(static_cast<unsigned>((vecs + 255) / 256)), dim3(256), 0, s,
-                   reinterpret_cast<const uint4*>(a.h), a.targets, a.dloss, vecs, static_cast<int>(a.d / 8), a.v,
-                   a.ignore_index, reinterpret_cast<uint4*>(ws));
-    if (e != cudaSuccess) return e;
-    scaled = reinterpret_cast<const uint16_t*>(ws);
-  }
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd>(num_sms, &max_clusters)) != cudaSuccess) return e;
   CUtensorMap th, tw, ths, dh_out, acc_out;
@@ -563,7 +566,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
                                         32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!rows_map(&dh_out, a.dh, a.d, a.t, a.d, 32) || !rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
-      !rows_map(&ths, scaled, a.d, a.t, a.d, 64))
+      !rows_map(&ths, scaled ? scaled : a.h, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
   for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
@@ -578,6 +581,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
+    p.h = a.h, p.scaled = i < 0 ? scaled : nullptr;
     p.status = a.status;
     CUtensorMap tz = th;
     p.dz_out = p.dw_out = p.acc_out = p.dh_out = dh_out;
