@@ -237,11 +237,12 @@ __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s
     }
   mtop = warp_top(mtop);
   vtop = warp_top(vtop);
-  const float mi = mtop >= kFlush ? __fdiv_rn(kFp8Max, mtop) : 0.0f;
-  const float vi = vtop >= kFlush ? __fdiv_rn(kFp8Max, vtop) : 0.0f;
+  // pinned like the moments: 448 times the reciprocal, and the top times 1 / 448
+  const float mi = mtop >= kFlush ? __fmul_rn(kFp8Max, __frcp_rn(mtop)) : 0.0f;
+  const float vi = vtop >= kFlush ? __fmul_rn(kFp8Max, __frcp_rn(vtop)) : 0.0f;
   if (lane == 0) {
-    t.m_scale[block] = mtop >= kFlush ? __fdiv_rn(mtop, kFp8Max) : 0.0f;
-    t.v_scale[block] = vtop >= kFlush ? __fdiv_rn(vtop, kFp8Max) : 0.0f;
+    t.m_scale[block] = mtop >= kFlush ? __fmul_rn(mtop, 1.0f / kFp8Max) : 0.0f;
+    t.v_scale[block] = vtop >= kFlush ? __fmul_rn(vtop, 1.0f / kFp8Max) : 0.0f;
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -315,7 +316,7 @@ cudaError_t launch_adamw(const sbl_adamw_tensor* tensors, int count, const sbl_a
   if (count < 1 || count > kAdamMaxTensors) return cudaErrorInvalidValue;
   const bool eight = (tensors[0].flags & SBL_ADAMW_STATE_8BIT) != 0u;
   const uint64_t chunk = static_cast<uint64_t>(chunk_of(eight));
-  AdamLaunch p = {};
+  AdamLaunch p;  // entries and first chunks past `count` are not read
   uint64_t chunks = 0;
   for (int i = 0; i < count; ++i) {
     const sbl_adamw_tensor& t = tensors[i];

@@ -2,6 +2,7 @@
 // entropy): argument checks and dispatch.  See include/sbl.h for the contract.
 #include <algorithm>
 #include <cmath>
+#include <functional>
 #include <new>
 #include <vector>
 
@@ -117,7 +118,9 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
       ws.push_back(t.w);
     }
     if (ws.empty()) return SBL_OK;
-    std::sort(ws.begin(), ws.end());
+    // ascending addresses, as an allocator gives them, need no sorting
+    if (std::adjacent_find(ws.begin(), ws.end(), std::greater_equal<const void*>()) != ws.end())
+      std::sort(ws.begin(), ws.end());
     if (std::adjacent_find(ws.begin(), ws.end()) != ws.end()) return SBL_ERR_INVALID_ARG;  // the same tensor twice
     int sms = 0;
     const sbl_status st = current_device(&sms);

@@ -415,15 +415,15 @@ def _addr(what: str, name: str, t, dtypes, numel: int, dev: int):
     """The address of tensor `t` after its checks; None stays None (the library refuses a NULL it needs)."""
     if t is None:
         return None
+    if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and t.numel() == numel:
+        return t.data_ptr()
     if t.dtype not in dtypes:
         raise SblError(SBL_ERR_INVALID_ARG, f"{what}: {name} is {t.dtype}, not one of {dtypes}")
     if t.get_device() != dev:
         raise SblError(SBL_ERR_DEVICE, f"{what}: {name} is on {t.device}, the call on CUDA device {dev}")
     if not t.is_contiguous():
         raise SblError(SBL_ERR_SHAPE, f"{what}: {name} is not dense")
-    if t.numel() != numel:
-        raise SblError(SBL_ERR_SHAPE, f"{what}: {name} has {t.numel()} elements, not {numel}")
-    return t.data_ptr()
+    raise SblError(SBL_ERR_SHAPE, f"{what}: {name} has {t.numel()} elements, not {numel}")
 
 
 def _room(T: _Types, what: str, t, nbytes: int, dev: int):
@@ -447,13 +447,12 @@ def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h
     T, me, n = _torch_types(), "sbl_rmsnorm_forward", t * k
     dev = _device(T, me, "x", x)
     xp = _addr(me, "x", x, T.float, n, dev)
-    rp = _addr(me, "residual", residual, T.float, n, dev)
-    wp = _addr(me, "weight", weight, T.float, k, dev)
-    stream_type = (x.dtype,) if residual is None else (residual.dtype,)
-    flags = ((SBL_NORM_X_F32 if x.dtype in T.f32 else 0) | (SBL_NORM_STREAM_F32 if stream_type == T.f32 else 0)
+    stream_type = T.f32 if (x if residual is None else residual).dtype in T.f32 else T.bf16
+    flags = ((SBL_NORM_X_F32 if x.dtype in T.f32 else 0) | (SBL_NORM_STREAM_F32 if stream_type is T.f32 else 0)
              | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
     code = lib().sbl_rmsnorm_forward(
-        xp, rp, wp, t, k, eps, flags, _addr(me, "h_out", h_out, stream_type, n, dev),
+        xp, _addr(me, "residual", residual, stream_type, n, dev), _addr(me, "weight", weight, T.float, k, dev),
+        t, k, eps, flags, _addr(me, "h_out", h_out, stream_type, n, dev),
         _addr(me, "xn_out", xn_out, T.bf16, n, dev), _addr(me, "xhat_out", xhat_out, T.bf16, n, dev),
         _addr(me, "xq_out", xq_out, T.i8, n, dev), _addr(me, "xscale_out", xscale_out, T.f32, t, dev),
         _addr(me, "rstd_out", rstd_out, T.f32, t, dev), _addr(me, "status", status, T.i32, 1, dev),

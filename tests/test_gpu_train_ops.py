@@ -396,6 +396,30 @@ def test_adamw_sizes(bits, gt, master):
     assert st.item() == 0
 
 
+def test_adamw_8bit_states_equal_a_plain_form_bit_for_bit():
+    """The moments' roundings are pinned (every product and sum by itself, the quotients through a reciprocal), so
+    the codes, which sit behind one more rounding, are the same in any fp32 form written that way."""
+    n = 64 * BLOCK
+    t = adam_tensor(n, 8, BF, True, True, 11)
+    plan = sbl.AdamWTensors([t])
+    c = {k: torch.tensor(v, device="cuda", dtype=F32) for k, v in
+         dict(b1=0.9, a1=1 - 0.9, b2=0.95, a2=1 - 0.95, up=448.0, low=2.0 ** -9).items()}
+    down = torch.ones((), device="cuda") / c["up"]
+    for step in range(1, 6):
+        m, r = (x.float().view(-1, BLOCK) * s[:, None] for x, s in ((t.m, t.m_scale), (t.v, t.v_scale)))
+        g = t.grad.float().view(-1, BLOCK)
+        m = c["b1"] * m + c["a1"] * g
+        r = (c["b2"] * (r * r) + c["a2"] * g * g).sqrt()
+        sbl.adamw_step(plan, step, **HYPER)
+        for x, codes, scales in ((m, t.m, t.m_scale), (r, t.v, t.v_scale)):
+            top = x.abs().amax(1)
+            assert same_bits(scales, top * down)
+            q = x * (top.reciprocal() * c["up"])[:, None]
+            if codes is t.v:
+                q = torch.where(q > 0, torch.maximum(q, c["low"]), q)
+            assert same_bits(codes.view(torch.int8), q.to(torch.float8_e4m3fn).view(-1).view(torch.int8))
+
+
 def test_adamw_mixed_tensors_over_several_launches():
     ts = []
     for i in range(300):
