@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "f32x2.cuh"
 #include "sbl_device.cuh"
 #include "sbl_kernels.h"
 
@@ -125,20 +126,45 @@ __device__ __forceinline__ void store4_bf16(void* base, int64_t i, const float (
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Four e4m3 codes of a word.
-__device__ __forceinline__ void from_fp8(uint32_t word, float (&f)[4]) {
+// The four e4m3 codes of a word, as two pairs.
+__device__ __forceinline__ void from_fp8(uint32_t word, f32x2 (&f)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(word >> (16 * h)), __NV_E4M3);
     const float2 v = __half22float2(__half2(raw));
-    f[2 * h] = v.x, f[2 * h + 1] = v.y;
+    f[h] = pair(v.x, v.y);
   }
 }
 
-__device__ __forceinline__ uint32_t to_fp8(const float (&f)[4]) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[0], f[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[2], f[3]), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t to_fp8(f32x2 a, f32x2 b) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(halves(a), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(halves(b), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
+}
+
+__device__ __forceinline__ float rsqrt_fast(float x) {
+  float y;
+  asm("rsqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The sum of two rounded products.  Scalar additions: a packed one behind a
+// packed product was seen to become one fused multiply-add, with one rounding less.
+__device__ __forceinline__ f32x2 sum_of_products(f32x2 a, f32x2 b) {
+  const float2 p = halves(a), q = halves(b);
+  return pair(__fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y));
+}
+
+// Square roots of two values from 2^-100 up, by Newton's step on g = v y with
+// y near 1 / sqrt(v) (Markstein, IBM J. Res. Dev. 1990): r = g + (v - g^2) y / 2,
+// the residual exact in a fused multiply-add.  The result before its rounding
+// is within 2^-44 (relative), so it is the rounded root but for about one value
+// in two million, there its neighbour.
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+  const float2 f = halves(v);
+  const f32x2 y = pair(rsqrt_fast(f.x), rsqrt_fast(f.y));
+  const f32x2 g = mul2(v, y), half = mul2(y, pair(0.5f, 0.5f));
+  return fma2(fma2(mul2(g, pair(-1.0f, -1.0f)), g, v), half, g);
 }
 
 template <bool GF32, bool MASTER>
@@ -184,27 +210,26 @@ __device__ __forceinline__ float warp_top(float top) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
-// A block of 256 elements by one warp, 8 consecutive ones a lane.
+// A block of 256 elements by one warp, 8 consecutive ones a lane, in pairs.
 template <bool GF32, bool MASTER>
 __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s, int64_t first, uint32_t& bad) {
   const int lane = threadIdx.x & 31;
   const int64_t start = first + (threadIdx.x >> 5) * SBL_ADAMW_BLOCK;
   if (start >= t.numel) return;
-  const int64_t block = start / SBL_ADAMW_BLOCK;
-  uint8_t* mp = static_cast<uint8_t*>(t.m);
-  uint8_t* vp = static_cast<uint8_t*>(t.v);
-  const int64_t i = start + 8 * lane;
+  const int64_t block = start / SBL_ADAMW_BLOCK, i = start + 8 * lane;
+  uint8_t* mp = static_cast<uint8_t*>(t.m) + i;
+  uint8_t* vp = static_cast<uint8_t*>(t.v) + i;
   const bool full = start + SBL_ADAMW_BLOCK <= t.numel;
-  float g[2][4], m[2][4], v[2][4], x[2][4];
+  float gf[2][4], xf[2][4];
   uint2 mw = make_uint2(0, 0), vw = make_uint2(0, 0);
   const float ms = t.m_scale[block], vs = t.v_scale[block];
   if (full) {
-    mw = *reinterpret_cast<const uint2*>(mp + i);
-    vw = *reinterpret_cast<const uint2*>(vp + i);
+    mw = *reinterpret_cast<const uint2*>(mp);
+    vw = *reinterpret_cast<const uint2*>(vp);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      load4<GF32>(t.grad, i + 4 * h, g[h]);
-      load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i + 4 * h, x[h]);
+      load4<GF32>(t.grad, i + 4 * h, gf[h]);
+      load4<MASTER>(MASTER ? static_cast<const void*>(t.master) : t.w, i + 4 * h, xf[h]);
     }
   } else {
 #pragma unroll
@@ -213,54 +238,94 @@ __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s
       for (int e = 0; e < 4; ++e) {
         const int64_t j = i + 4 * h + e;
         const bool in = j < t.numel;
-        g[h][e] = in ? load1(t.grad, j, GF32) : 0.0f;
-        x[h][e] = in ? (MASTER ? t.master[j] : load1(t.w, j, false)) : 0.0f;
-        (h ? mw.y : mw.x) |= in ? uint32_t(mp[j]) << (8 * e) : 0u;
-        (h ? vw.y : vw.x) |= in ? uint32_t(vp[j]) << (8 * e) : 0u;
+        gf[h][e] = in ? load1(t.grad, j, GF32) : 0.0f;
+        xf[h][e] = in ? (MASTER ? t.master[j] : load1(t.w, j, false)) : 0.0f;
+        (h ? mw.y : mw.x) |= in ? uint32_t(mp[4 * h + e]) << (8 * e) : 0u;
+        (h ? vw.y : vw.x) |= in ? uint32_t(vp[4 * h + e]) << (8 * e) : 0u;
       }
   }
-  from_fp8(mw.x, m[0]);
-  from_fp8(mw.y, m[1]);
-  from_fp8(vw.x, v[0]);
-  from_fp8(vw.y, v[1]);
-  float mtop = 0.0f, vtop = 0.0f;
+  f32x2 m[4], v[4];
+  {
+    f32x2 a[2], b[2];
+    from_fp8(mw.x, a);
+    from_fp8(mw.y, b);
+    m[0] = a[0], m[1] = a[1], m[2] = b[0], m[3] = b[1];
+    from_fp8(vw.x, a);
+    from_fp8(vw.y, b);
+    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+  }
+  float mtop = 0.0f;
+  uint32_t vtop = 0, vlow = 0x7F800000u;  // the second moments' bits, which order as they do
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      m[h][e] = __fmul_rn(m[h][e], ms);
-      v[h][e] = __fmul_rn(v[h][e], vs);
-      v[h][e] = __fmul_rn(v[h][e], v[h][e]);
-      v[h][e] = adam_element(s, g[h][e], m[h][e], v[h][e], x[h][e], bad);
-      mtop = fmaxf(mtop, fabsf(m[h][e]));
-      vtop = fmaxf(vtop, v[h][e]);
-    }
+  for (int e = 0; e < 4; ++e) {
+    const f32x2 g = mul2(pair(gf[e >> 1][2 * (e & 1)], gf[e >> 1][2 * (e & 1) + 1]), pair(s.scale, s.scale));
+    m[e] = sum_of_products(mul2(pair(s.b1, s.b1), mul2(m[e], pair(ms, ms))), mul2(pair(s.one_b1, s.one_b1), g));
+    v[e] = mul2(v[e], pair(vs, vs));
+    v[e] = sum_of_products(mul2(pair(s.b2, s.b2), mul2(v[e], v[e])), mul2(mul2(pair(s.one_b2, s.one_b2), g), g));
+    const float2 a = halves(m[e]), b = halves(v[e]);
+    mtop = fmaxf(mtop, fmaxf(fabsf(a.x), fabsf(a.y)));
+    const uint32_t b0 = __float_as_uint(b.x), b1 = __float_as_uint(b.y);
+    vtop = max(vtop, max(b0, b1));
+    vlow = min(vlow, min(b0, b1));
+  }
   mtop = warp_top(mtop);
-  vtop = warp_top(vtop);
+  vtop = __reduce_max_sync(0xffffffffu, vtop);
+  bad = max(bad, vtop);
+  const float rtop = __fsqrt_rn(__uint_as_float(vtop));
   // pinned like the moments: 448 times the reciprocal, and the top times 1 / 448
   const float mi = mtop >= kFlush ? __fmul_rn(kFp8Max, __frcp_rn(mtop)) : 0.0f;
-  const float vi = vtop >= kFlush ? __fmul_rn(kFp8Max, __frcp_rn(vtop)) : 0.0f;
+  const float vi = rtop >= kFlush ? __fmul_rn(kFp8Max, __frcp_rn(rtop)) : 0.0f;
   if (lane == 0) {
     t.m_scale[block] = mtop >= kFlush ? __fmul_rn(mtop, 1.0f / kFp8Max) : 0.0f;
-    t.v_scale[block] = vtop >= kFlush ? __fmul_rn(vtop, 1.0f / kFp8Max) : 0.0f;
+    t.v_scale[block] = rtop >= kFlush ? __fmul_rn(rtop, 1.0f / kFp8Max) : 0.0f;
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
+  // Where no root is below a smallest code (448 2^-9 of the top: 2^-36 of the
+  // top's square, with room) nor outside root2's range, none needs a look.
+  f32x2 r[4];
+  const float low = __uint_as_float(vlow);
+  const bool plain = low >= 0x1p-100f && low >= 0x1p-34f * __uint_as_float(vtop);
+  if (__all_sync(0xffffffffu, plain)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      m[h][e] = __fmul_rn(m[h][e], mi);
-      v[h][e] = __fmul_rn(v[h][e], vi);
-      if (v[h][e] > 0.0f) v[h][e] = fmaxf(v[h][e], kFp8Min);
+      r[e] = root2(v[e]);
+      v[e] = mul2(r[e], pair(vi, vi));
     }
-  mw = make_uint2(to_fp8(m[0]), to_fp8(m[1]));
-  vw = make_uint2(to_fp8(v[0]), to_fp8(v[1]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = halves(v[e]), b = make_float2(__fsqrt_rn(a.x), __fsqrt_rn(a.y));
+      r[e] = pair(b.x, b.y);
+      float q0 = __fmul_rn(b.x, vi), q1 = __fmul_rn(b.y, vi);
+      if (q0 > 0.0f) q0 = fmaxf(q0, kFp8Min);
+      if (q1 > 0.0f) q1 = fmaxf(q1, kFp8Min);
+      v[e] = pair(q0, q1);
+    }
+  }
+  f32x2 x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 den = halves(fma2(r[e], pair(s.inv_root, s.inv_root), pair(s.eps, s.eps)));
+    const float2 num = halves(mul2(m[e], pair(-s.rate, -s.rate)));
+    // the quotients are off by two units at most; nothing rounds behind them
+    x[e] = fma2(pair(xf[e >> 1][2 * (e & 1)], xf[e >> 1][2 * (e & 1) + 1]), pair(s.keep, s.keep),
+                pair(__fdividef(num.x, den.x), __fdividef(num.y, den.y)));
+    m[e] = mul2(m[e], pair(mi, mi));
+  }
+  mw = make_uint2(to_fp8(m[0], m[1]), to_fp8(m[2], m[3]));
+  vw = make_uint2(to_fp8(v[0], v[1]), to_fp8(v[2], v[3]));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 a = halves(x[e]);
+    xf[e >> 1][2 * (e & 1)] = a.x;
+    xf[e >> 1][2 * (e & 1) + 1] = a.y;
+  }
   if (full) {
-    *reinterpret_cast<uint2*>(mp + i) = mw;
-    *reinterpret_cast<uint2*>(vp + i) = vw;
+    *reinterpret_cast<uint2*>(mp) = mw;
+    *reinterpret_cast<uint2*>(vp) = vw;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (MASTER) store4(t.master, i + 4 * h, x[h]);
-      store4_bf16(t.w, i + 4 * h, x[h]);
+      if (MASTER) store4(t.master, i + 4 * h, xf[h]);
+      store4_bf16(t.w, i + 4 * h, xf[h]);
     }
   } else {
 #pragma unroll
@@ -269,10 +334,10 @@ __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s
       for (int e = 0; e < 4; ++e) {
         const int64_t j = i + 4 * h + e;
         if (j >= t.numel) continue;
-        mp[j] = static_cast<uint8_t>((h ? mw.y : mw.x) >> (8 * e));
-        vp[j] = static_cast<uint8_t>((h ? vw.y : vw.x) >> (8 * e));
-        if (MASTER) t.master[j] = x[h][e];
-        static_cast<__nv_bfloat16*>(t.w)[j] = __float2bfloat16_rn(x[h][e]);
+        mp[4 * h + e] = static_cast<uint8_t>((h ? mw.y : mw.x) >> (8 * e));
+        vp[4 * h + e] = static_cast<uint8_t>((h ? vw.y : vw.x) >> (8 * e));
+        if (MASTER) t.master[j] = xf[h][e];
+        static_cast<__nv_bfloat16*>(t.w)[j] = __float2bfloat16_rn(xf[h][e]);
       }
   }
 }

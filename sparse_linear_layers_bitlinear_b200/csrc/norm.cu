@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 
 #include "actq_math.cuh"
+#include "f32x2.cuh"
 #include "sbl_device.cuh"
 #include "sbl_kernels.h"
 
@@ -76,34 +77,6 @@ struct NormParams {
 // Residual types of the forward kernel.
 enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
-// Two fp32 values in a register pair: sm_100's packed fp32 instructions, each
-// half rounded as the scalar ones do.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 halves(f32x2 v) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
-  return d;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
 __device__ __forceinline__ f32x2 unpack2(uint32_t w) {
   return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }

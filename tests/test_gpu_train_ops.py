@@ -399,7 +399,7 @@ def test_adamw_sizes(bits, gt, master):
 def test_adamw_8bit_states_equal_a_plain_form_bit_for_bit():
     """The moments' roundings are pinned (every product and sum by itself, the quotients through a reciprocal), so
     the codes, which sit behind one more rounding, are the same in any fp32 form written that way."""
-    n = 64 * BLOCK
+    n = 1000 * BLOCK
     t = adam_tensor(n, 8, BF, True, True, 11)
     plan = sbl.AdamWTensors([t])
     c = {k: torch.tensor(v, device="cuda", dtype=F32) for k, v in
