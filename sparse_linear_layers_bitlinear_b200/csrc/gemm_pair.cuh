@@ -66,6 +66,17 @@ struct PairOut<Cfg, decltype(void(Cfg::OUT_BYTES))> {
   static constexpr int bytes = Cfg::OUT_BYTES;
 };
 
+// Configurations that let the kernel behind them launch at once (EARLY_TRIGGER):
+// it sets up on SMs that this launch leaves free and waits there.
+template <class Cfg, class = void>
+struct PairEarly {
+  static constexpr bool value = false;
+};
+template <class Cfg>
+struct PairEarly<Cfg, decltype(void(Cfg::EARLY_TRIGGER))> {
+  static constexpr bool value = Cfg::EARLY_TRIGGER;
+};
+
 // Configurations whose tiles are of MMA_KINDS kinds have the loop over a tile's
 // stages compiled for each.
 template <int KIND>
@@ -104,6 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   uint32_t* status = p.status;
+  if constexpr (PairEarly<Cfg>::value) pdl_trigger();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < Cfg::STAGES; ++s) {

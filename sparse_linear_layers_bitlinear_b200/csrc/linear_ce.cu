@@ -40,7 +40,7 @@ __device__ __forceinline__ float exp_of(float x) {  // exp(x), x <= 0 or slightl
 template <class P>
 struct CfgCeLogits {
   using Params = P;
-  static constexpr bool QUANT_X = false;
+  static constexpr bool QUANT_X = false, EARLY_TRIGGER = true;
   static constexpr int MAPS = 2;
   static constexpr int EPI_WARPS = 4, PARTS = EPI_WARPS / 4;
   static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
@@ -211,7 +211,7 @@ struct CeBwdParams {
 
 struct CfgCeBwd {
   using Params = CeBwdParams;
-  static constexpr bool QUANT_X = false;
+  static constexpr bool QUANT_X = false, EARLY_TRIGGER = true;
   static constexpr int MAPS = 4;
   static constexpr int EPI_WARPS = 4;
   static constexpr int BN = kCeTile, BK = 64, STAGES = 6;

@@ -430,7 +430,7 @@ struct NormBwdParams {
   float* part;  // [gridDim.x][k], or nullptr without dw
 };
 
-constexpr int kNormBwdThreads = 640;
+constexpr int kNormBwdThreads = 512, kNormBwdRuns = 5;  // of a block; runs of 256 elements a warp at most
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* smem, const void* gmem) {
@@ -502,7 +502,7 @@ __device__ __forceinline__ void store8_bf16(void* base, int64_t el, const uint4 
 }
 
 template <bool HF32, bool DF32, int R, bool RING>
-__global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_bwd(const NormBwdParams p) {
+__global__ void __launch_bounds__(kNormBwdThreads, 1) k_rmsnorm_bwd(const NormBwdParams p) {
   constexpr int HW = HF32 ? 2 : 1, DW = DF32 ? 2 : 1;
   constexpr bool QUADS = HF32 || DF32;
   extern __shared__ uint4 s_ring[];
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
   if constexpr (RING)  // words that no copy fills (past the row's end) stay zero
     for (int i = 0; i < p.depth * p.words; ++i) mine[i * 32] = make_uint4(0, 0, 0, 0);
   float* const s_w = reinterpret_cast<float*>(s_ring + (blockDim.x >> 5) * p.depth * p.words * 32);
-  if constexpr (R <= 2)
+  if constexpr (RING)
     if (p.w != nullptr) {
       for (int i = threadIdx.x; i < p.warps * R * 32; i += blockDim.x) {
         float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
       copy_commit();
     }
   }
-  if constexpr (R <= 2) __syncthreads();  // the weight
+  if constexpr (RING) __syncthreads();  // the weight
 
   int slot = 0, parity = 0;
   float rstd_next = first < p.t ? p.rstd[first] : 0.0f;
@@ -604,11 +604,11 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
     }
     uint4* const src = mine + slot * slot_step;
     const f32x2 rstd2 = pair(rstd, rstd);
-    f32x2 n[R][4], g[R][4], c2 = pair(0.0f, 0.0f);
+    f32x2 g[R][4], c2 = pair(0.0f, 0.0f);  // n is formed again below: its registers hold more rows instead
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      f32x2 u[4];
-      h_at(src, 0, p.h, el, r).unpack(n[r]);
+      f32x2 u[4], n[4];
+      h_at(src, 0, p.h, el, r).unpack(n);
       d_at(src, kDy, p.dy[0], el, r).unpack(g[r]);
       if (p.ndy > 1) {
         d_at(src, kDy + kOne, p.dy[1], el, r).unpack(u);
@@ -622,11 +622,11 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        n[r][e] = mul2(n[r][e], rstd2);
-        acc[r][e] = fma2(g[r][e], n[r][e], acc[r][e]);
+        n[e] = mul2(n[e], rstd2);
+        acc[r][e] = fma2(g[r][e], n[e], acc[r][e]);
       }
       if (p.w != nullptr) {
-        if constexpr (R <= 2) {
+        if constexpr (RING) {
           const float4* w = reinterpret_cast<const float4*>(s_w + at + r * 256);
           const float4 a = w[0], b = w[QUADS ? 32 : 1];
           u[0] = pair(a.x, a.y), u[1] = pair(a.z, a.w), u[2] = pair(b.x, b.y), u[3] = pair(b.z, b.w);
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
         for (int e = 0; e < 4; ++e) g[r][e] = mul2(g[r][e], u[e]);
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c2 = fma2(g[r][e], n[r][e], c2);
+      for (int e = 0; e < 4; ++e) c2 = fma2(g[r][e], n[e], c2);
     }
     const float2 ch = halves(c2);
     float c = ch.x + ch.y;
@@ -657,9 +657,10 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
     const f32x2 minus = pair(c, c);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      f32x2 d[4];
+      f32x2 d[4], n[4];
+      h_at(src, 0, p.h, el, r).unpack(n);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = mul2(rstd2, fma2(n[r][e], minus, g[r][e]));
+      for (int e = 0; e < 4; ++e) d[e] = mul2(rstd2, fma2(mul2(n[e], rstd2), minus, g[r][e]));
       if (p.dres != nullptr) {
         f32x2 u[4];
         h_at(src, kRes, p.dres, el, r).unpack(u);
@@ -685,33 +686,35 @@ __global__ void __launch_bounds__(R <= 2 ? kNormBwdThreads : 512, 1) k_rmsnorm_b
     }
   }
   if (p.part == nullptr) return;
-  float* dst = p.part + int64_t(blockIdx.x) * k;
-  float* sum = reinterpret_cast<float*>(s_ring);
+  // the groups' shares side by side, then added in the groups' order
+  float* const dst = p.part + int64_t(blockIdx.x) * k;
+  float* const share = p.groups > 1 ? reinterpret_cast<float*>(s_ring) + group * k : dst;
   copy_wait<0>();
   if (p.groups > 1) __syncthreads();  // every group is done with the ring
-  for (int gr = 0; gr < p.groups; ++gr) {  // the groups' shares, one group after the other
-    if (p.groups > 1) __syncthreads();
-    if (group != gr) continue;
-    float* to = gr == p.groups - 1 ? dst : sum;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int i = at + r * 256 + q * (QUADS ? 128 : 4);
-        if (!(q ? in1[r] : in0[r])) continue;
-        const float2 a0 = halves(acc[r][2 * q]), a1 = halves(acc[r][2 * q + 1]);
-        float4 a = make_float4(a0.x, a0.y, a1.x, a1.y);
-        if (gr > 0) {
-          const float4 u = *reinterpret_cast<const float4*>(sum + i);
-          a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-        }
-        *reinterpret_cast<float4*>(to + i) = a;
-      }
+    for (int q = 0; q < 2; ++q) {
+      if (!(q ? in1[r] : in0[r])) continue;
+      const float2 a0 = halves(acc[r][2 * q]), a1 = halves(acc[r][2 * q + 1]);
+      *reinterpret_cast<float4*>(share + at + r * 256 + q * (QUADS ? 128 : 4)) = make_float4(a0.x, a0.y, a1.x, a1.y);
+    }
+  if (p.groups == 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.nvec; i += blockDim.x) {
+    const float4* src = reinterpret_cast<const float4*>(s_ring) + i;
+    float4 a = src[0];
+    for (int g = 1; g < p.groups; ++g) {
+      const float4 b = src[g * 2 * p.nvec];
+      a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+    }
+    reinterpret_cast<float4*>(dst)[i] = a;
   }
 }
 
-// dw[c] = sum of the blocks' partial sums: 8 threads of 4 columns across, 32 rows of
-// partial sums at a time, then a tree over the 32.
+// dw[c] = sum of the blocks' partial sums: 8 threads of 4 columns across, 32
+// rows of partial sums beside each other (at most 8 each, all loads at once),
+// then a tree over the 32.
 __global__ void __launch_bounds__(256) k_norm_dw(const float4* __restrict__ part, int blocks, int n4, float4* dw) {
   __shared__ float4 s[32][8];
   pdl_wait();
@@ -719,19 +722,27 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float4* __restrict__ part
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int col = blockIdx.x * 8 + x;
   float4 a = make_float4(0, 0, 0, 0);
-  if (col < n4)
-    for (int b = y; b < blocks; b += 32) {
-      const float4 v = __ldcg(part + int64_t(b) * n4 + col);
-      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+  if (col < n4) {
+    float4 v[kNormBwdMaxBlocks / 32];
+#pragma unroll
+    for (int i = 0; i < kNormBwdMaxBlocks / 32; ++i) {
+      const int b = y + 32 * i;
+      v[i] = b < blocks ? __ldcg(part + int64_t(b) * n4 + col) : make_float4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < kNormBwdMaxBlocks / 32; ++i) a.x += v[i].x, a.y += v[i].y, a.z += v[i].z, a.w += v[i].w;
+  }
   s[y][x] = a;
-  for (int o = 16; o > 0; o >>= 1) {
-    __syncthreads();
-    if (y < o) {
-      const float4 v = s[y + o][x];
-      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-      s[y][x] = a;
-    }
+  __syncthreads();
+  if (y >= 4) return;  // one warp: four rows of eight columns
+  for (int i = y + 4; i < 32; i += 4) {
+    const float4 v = s[i][x];
+    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+  }
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    a.x += __shfl_down_sync(0xffffffffu, a.x, o), a.y += __shfl_down_sync(0xffffffffu, a.y, o);
+    a.z += __shfl_down_sync(0xffffffffu, a.z, o), a.w += __shfl_down_sync(0xffffffffu, a.w, o);
   }
   if (y == 0 && col < n4) dw[col] = a;
 }
@@ -744,37 +755,46 @@ cudaError_t launch_norm_bwd(const NormBwdParams& p, int blocks, size_t smem, cud
   return launch_pdl(k_rmsnorm_bwd<HF32, DF32, R, RING>, dim3(blocks), dim3(32 * p.warps * p.groups), smem, s, p);
 }
 
-// Two runs a warp (one where a warp holds the row, four where 20 warps do not),
-// and of the numbers of rows that a block can work on at a time the one with the
-// most rows in its ring, but no more than there are rows for all SMs; one block
-// an SM.
+// Warps a row and runs a warp: the fewest instructions for a row, of which a
+// warp spends some 180 beside 160 a run (8192 x 6912 in bf16: 7 warps of 4 runs
+// 75.5 us, 14 of 2 runs 126).  As many rows at a time as 14 warps hold, with the
+// most of them in the ring, but no more than there are rows for all SMs; one
+// block an SM.  The two warps' registers that are left hold blocks of the second
+// launch, which then start at once (4096 x 2560, three gradients: 28.5 -> 27.0 us).
 template <bool HF32, bool DF32>
 cudaError_t pick_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t s) {
-  const int r = p.nvec <= 32 ? 1 : p.nvec <= 1024 ? 2 : 4;
-  const int most_warps = (r <= 2 ? kNormBwdThreads : 512) / 32;
-  p.warps = (p.nvec + 32 * r - 1) / (32 * r);
+  constexpr int most_warps = kNormBwdThreads / 32;
+  const auto up = [](int a, int b) { return (a + b - 1) / b; };
+  p.warps = up(p.nvec, 32 * kNormBwdRuns);
+  for (int w = p.warps + 1; w <= most_warps; ++w)
+    if (w * (180 + 160 * up(p.nvec, 32 * w)) < p.warps * (180 + 160 * up(p.nvec, 32 * p.warps))) p.warps = w;
+  const int r = up(p.nvec, 32 * p.warps);
   p.words = r * ((HF32 ? 2 : 1) * 2 + (DF32 ? 2 : 1) * p.ndy);
-  const size_t weight = r <= 2 && p.w != nullptr ? size_t(p.warps) * r * 1024 : 0;  // fp32, behind the ring
+  const size_t weight = p.w != nullptr ? size_t(p.warps) * r * 1024 : 0;  // fp32, behind the ring
   const size_t room = 224 * 1024 - weight;
   const size_t one = size_t(p.words) * 16 * 32 * p.warps;
   const auto depth = [&](int groups) { return static_cast<int>(std::min<size_t>(room / (one * groups), 3)); };
-  const int most = static_cast<int>(std::min<int64_t>({most_warps / p.warps, 15, (p.t + num_sms - 1) / num_sms}));
+  const int most = static_cast<int>(std::min<int64_t>({std::max(14 / p.warps, 1), (p.t + num_sms - 1) / num_sms}));
   p.groups = most;
   for (int g = most - 1; g >= 1; --g)
     if (g * depth(g) > p.groups * depth(p.groups)) p.groups = g;
   p.depth = depth(p.groups);
-  const size_t row = one * p.groups;
-  const size_t smem = std::max<size_t>(p.depth * row + weight, p.groups > 1 ? size_t(p.nvec) * 32 : 0);
+  const size_t smem = std::max<size_t>(p.depth > 0 ? p.depth * one * p.groups + weight : 0,
+                                       p.groups > 1 ? size_t(p.groups) * p.nvec * 32 : 0);  // 80 KB at most
   const int blocks = static_cast<int>(std::min<int64_t>(p.t, num_sms));
   cudaError_t e;
-  if (r == 1)
+  if (p.depth == 0)  // not even one row fits: long fp32 rows of several arrays
+    e = launch_norm_bwd<HF32, DF32, kNormBwdRuns, false>(p, blocks, smem, s);
+  else if (r == 1)
     e = launch_norm_bwd<HF32, DF32, 1, true>(p, blocks, smem, s);
   else if (r == 2)
-    e = launch_norm_bwd<HF32, DF32, 2, true>(p, blocks, smem, s);  // a row takes 163,840 bytes at most
-  else if (p.depth > 0)
+    e = launch_norm_bwd<HF32, DF32, 2, true>(p, blocks, smem, s);
+  else if (r == 3)
+    e = launch_norm_bwd<HF32, DF32, 3, true>(p, blocks, smem, s);
+  else if (r == 4)
     e = launch_norm_bwd<HF32, DF32, 4, true>(p, blocks, smem, s);
   else
-    e = launch_norm_bwd<HF32, DF32, 4, false>(p, blocks, smem, s);
+    e = launch_norm_bwd<HF32, DF32, 5, true>(p, blocks, smem, s);
   if (e != cudaSuccess || dw == nullptr) return e;
   const int n4 = 2 * p.nvec;
   return launch_pdl(k_norm_dw, dim3((n4 + 7) / 8), dim3(256), 0, s, reinterpret_cast<const float4*>(p.part), blocks,
