@@ -32,8 +32,11 @@ namespace {
 
 constexpr int kCeTile = 256;
 
-__device__ __forceinline__ float exp_of(float x) {  // exp(x), x <= 0 or slightly above
-  return exp2f(x * 1.4426950408889634f);
+// exp(x) to about 2^-22 (relative), results below 2^-126 zero.
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
 }
 
 // Common form of the h . w^T tiles: A = h rows, B = w rows, both K-major.
@@ -106,18 +109,21 @@ struct CfgCeFwd : CfgCeLogits<CeFwdParams> {
       const int left = p.v - col0;
       const int64_t at = target - col0;
       const bool mine = in && at >= 0 && at < 32 && target < p.v;  // the target's logit is in this chunk
-      float z[32], best = top, hit = 0.0f;
+      // four maxima and four sums side by side: a single tile's latency is that of these chains
+      float z[32], best4[4] = {top, top, top, top}, sum4[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hit = 0.0f;
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         z[e] = e < left ? __uint_as_float(r[e]) : -INFINITY;
-        best = fmaxf(best, z[e]);
+        best4[e & 3] = fmaxf(best4[e & 3], z[e]);
         if (mine && e == int(at)) hit += z[e];
       }
       if (mine) p.hit[row] = hit;
+      const float best = fmaxf(fmaxf(best4[0], best4[1]), fmaxf(best4[2], best4[3]));
       const float base = best == -INFINITY ? 0.0f : best;
       sum *= exp_of(top - base);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) sum += exp_of(z[e] - base);
+      for (int e = 0; e < 32; ++e) sum4[e & 3] += exp_of(z[e] - base);
+      sum += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
       top = best;
     }
     if (in) p.piece[int64_t(row) * p.pieces + PARTS * (n0 / BN) + part] = make_float2(top, sum);
