@@ -342,8 +342,11 @@ sbl_status sbl_backward_ws(const sbl_layer* layer, const void* x, const void* dy
  * between sbl_forward / sbl_backward calls.  The paper has no counterpart for
  * them beyond naming the network they sit in.  Same conventions as above
  * (device pointers, caller-owned buffers, no synchronisation, capturable into
- * CUDA graphs).  `status_dev` is a caller-owned device uint32 or NULL (then
- * device-side errors are not reported).
+ * CUDA graphs).  `status_dev` is a caller-owned device uint32 that error bits
+ * are OR-ed into, or NULL (then device-side errors are not reported).  Outputs
+ * and workspaces overlap nothing else of a call unless an entry says so.  A
+ * workspace holds nothing between calls; calls that can overlap on the GPU (two
+ * streams, two captured graphs) need one each.
  * ------------------------------------------------------------------------- */
 
 /* Types of the operands of sbl_rmsnorm_forward / sbl_rmsnorm_backward; a
@@ -367,12 +370,12 @@ enum {
  * x, residual: [t, k]; weight: [k].  Outputs, each may be NULL, one at least
  * is wanted: h_out [t, k] (the stream's type; without a residual x's type),
  * xn_out and xhat_out bf16 [t, k], xq_out int8 [t, k], xscale_out fp32 [t],
- * rstd_out fp32 [t].  h_out may be `residual`; no other overlap of an output
- * with another argument.  k: a multiple of 8 up to SBL_NORM_MAX_K (of 64 when
+ * rstd_out fp32 [t].  h_out may be `residual`.  k: a multiple of 8 up to SBL_NORM_MAX_K (of 64 when
  * the codes are to enter sbl_forward_quantized); eps: 1e-12 to 1.  A row of
  * zeros gives xn = 0, xscale = 1e-5, xq = 0.  A non-finite h or xn raises
  * SBL_STATUS_NONFINITE_X; the other rows are not touched by it.  t == 0 is a
- * no-op. */
+ * no-op.  Errors: SBL_ERR_SHAPE (t, k), SBL_ERR_INVALID_ARG (eps, an unknown
+ * flag, no x, no output), SBL_ERR_ALIGN, SBL_ERR_DEVICE, SBL_ERR_CUDA. */
 sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* weight, int64_t t, int64_t k,
                                double eps, uint32_t flags, void* h_out, void* xn_out, void* xhat_out, int8_t* xq_out,
                                float* xscale_out, float* rstd_out, uint32_t* status_dev, sbl_stream_t stream);
@@ -389,7 +392,8 @@ sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* 
  * dh is the gradient of x and of residual alike.  h is the forward's h_out (or
  * its x, without a residual) in the stream's type.  dh may be dres.  dw needs
  * `workspace`, sbl_rmsnorm_backward_workspace_bytes(t, k) bytes, 16-byte
- * aligned; its sum has a fixed order.  t == 0: dw = 0. */
+ * aligned; its sum has a fixed order.  rstd needs 4-byte alignment only.
+ * t == 0: dw = 0.  Errors as the forward's. */
 sbl_status sbl_rmsnorm_backward(const void* h, const float* rstd, const void* weight, const void* const* dys,
                                 int32_t dy_count, const void* dres, int64_t t, int64_t k, uint32_t flags, void* dh,
                                 void* dx, float* dw, void* workspace, sbl_stream_t stream);
@@ -430,20 +434,24 @@ typedef struct sbl_adamw_params {
  *   g = grad grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   value -= lr weight_decay value;  value -= lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
  *   w = RN_bf16(value), value in `master` (or in w)
- * in fp32.  8-bit states: per block of 256 elements m = code m_scale and
- * sqrt(v) = code v_scale with e4m3 codes (float8_e4m3fn), the scale the
- * block's largest magnitude / 448; codes round to nearest, except that a
- * second moment above zero never becomes zero.  A block whose largest
- * magnitude is below 2^-100 holds zeros with scale 0.  The step itself uses
- * m and v before that rounding.  Nearest rounding moves a code only when its
- * value changes by about 3 to 6 %: use beta2 of 0.95 or so with 8-bit states, not
- * 0.999.  Zeroed states (scales too) are the start.  Tensors of a call must
- * not share memory (two entries with the same w: SBL_ERR_INVALID_ARG).
- * Alignment: w, master, grad, m and v 16 bytes, the scales 4.  A non-finite
- * gradient raises SBL_STATUS_NONFINITE_G; that tensor's block of 256 is then
- * unspecified.  numel 0 and count 0 are no-ops.  SBL_ERR_SHAPE: negative
- * numel or one above 2^40; SBL_ERR_INVALID_ARG: step < 1 (without step_dev),
- * a beta outside [0, 1), eps, lr or weight_decay negative or not finite. */
+ * in fp32, the moments' products and sums rounded one by one.
+ * 8-bit states: per block of 256 elements m = code m_scale and sqrt(v) = code
+ * v_scale with e4m3 codes (float8_e4m3fn); the scale is the block's largest
+ * magnitude times RN(1 / 448), the code that of the value times
+ * RN(448 RN(1 / largest)).  Codes round to nearest, except that a second moment
+ * above zero never becomes zero.  A block whose largest magnitude is below
+ * 2^-100 holds zeros with scale 0.  The step itself uses m and v before that
+ * rounding.  Nearest rounding moves a code only when its value changes by
+ * about 3 to 6 %: use beta2 of 0.95 or so with 8-bit states, not 0.999.
+ * Zeroed states (scales too) are the start.  Tensors of a call must not share
+ * memory (two entries with the same w: SBL_ERR_INVALID_ARG).  Alignment: w,
+ * master, grad, m and v 16 bytes, the scales 4.  A gradient that is not finite
+ * (or, with 8-bit states, whose square is not) raises SBL_STATUS_NONFINITE_G;
+ * that element, or its block of 256, is then unspecified.  *step_dev must be 1
+ * or more.  numel 0 and count 0 are no-ops.  Errors: SBL_ERR_SHAPE (numel
+ * negative or above 2^40); SBL_ERR_INVALID_ARG (a NULL pointer, an unknown flag,
+ * step < 1 without step_dev, a beta outside [0, 1), eps, lr or weight_decay
+ * negative or not finite); SBL_ERR_ALIGN, SBL_ERR_DEVICE, SBL_ERR_CUDA. */
 sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const sbl_adamw_params* params,
                           uint32_t* status_dev, sbl_stream_t stream);
 
@@ -453,9 +461,12 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
  * without loss (loss 0; lse is still written).  loss, lse: fp32 [t].  d: a
  * multiple of 8 up to 131072; v >= 1 and t up to 2^22.  A target outside
  * [0, v) that is not ignore_index gives loss NaN and raises
- * SBL_STATUS_BAD_TARGET.  targets, loss, lse and dloss need only their
+ * SBL_STATUS_BAD_TARGET; a bounded wait that ran out raises
+ * SBL_STATUS_TIMEOUT, here and in the backward pass.  targets, loss, lse and dloss need only their
  * elements' own alignment.  `workspace`: sbl_linear_ce_workspace_bytes(t, v, d,
- * 0) bytes, 256-byte aligned.  t == 0 is a no-op. */
+ * 0) bytes, 256-byte aligned.  t == 0 is a no-op.  Errors: SBL_ERR_SHAPE (t, v,
+ * d), SBL_ERR_INVALID_ARG (a NULL pointer), SBL_ERR_ALIGN, SBL_ERR_DEVICE,
+ * SBL_ERR_CUDA. */
 sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* targets, int64_t t, int64_t v, int64_t d,
                                  int64_t ignore_index, float* loss, float* lse, void* workspace, uint32_t* status_dev,
                                  sbl_stream_t stream);
@@ -465,10 +476,13 @@ sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* ta
  *   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]), 0 for ignored rows and rows with a bad target
  *   dh = dz w  bf16 [t, d],   dw = dz^T h  bf16 [v, d]
  * The logits are computed again, a piece of the vocabulary at a time.  For the
- * two products, which accumulate in fp32, exp(z - lse) - [j = target] is
- * rounded to bf16, and for dw also dloss_i h_i (not with stride 0).
+ * two products, which accumulate in fp32, dz is rounded to bf16 below 2048
+ * entries; from there on exp(z - lse) - [j = target] is, and for dw also
+ * dloss_i h_i (with stride 0: dloss multiplies the sums in either range).
  * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 1) bytes, 256-byte
- * aligned.  t == 0: dw = 0. */
+ * aligned.  Rows without loss give dh = 0 whatever their lse and dloss hold.
+ * t == 0: dw = 0.  Errors: as the forward, plus SBL_ERR_INVALID_ARG for a
+ * dloss_stride other than 0 and 1. */
 sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,
                                   const float* dloss, int64_t dloss_stride, int64_t t, int64_t v, int64_t d,
                                   int64_t ignore_index, void* dh, void* dw, void* workspace, uint32_t* status_dev,

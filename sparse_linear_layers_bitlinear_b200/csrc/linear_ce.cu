@@ -5,10 +5,11 @@
 //   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]),  dh = dz w,  dw = dz^T h
 //
 // Forward: a tile of 256 tokens x 256 vocabulary entries leaves, per token, its
-// largest logit and the sum of the exponentials below it (the epilogue's eight
-// warps keep a half tile each); a second launch joins a token's pieces.  The
-// product bounds it: 2 t v d flops; the exponentials (one per logit) run on
-// the epilogue warps under the next tile's product.
+// largest logit and the sum of the exponentials below it; a second launch joins
+// a token's pieces.  The product bounds it: 2 t v d flops; the exponentials (one
+// per logit) run on the epilogue warps under the next tile's product.  Measured,
+// sustained (the power cap holds the clock), 8192 x 32768 x 2560: 1020 us, 1350
+// TFLOP/s; the library's product alone, with its logits written: 1010 us.
 //
 // Backward, a piece of the vocabulary at a time, so that dz (bf16, at most
 // kCeDzBytes) stays in L2 between its writer and its two readers: a launch
@@ -16,6 +17,9 @@
 // the piece before.  dw rows belong to one piece; dh adds up over the pieces
 // in fp32.  With few tokens dh has few output tiles and a long sum over the
 // vocabulary, which is then split over slices that a last launch joins.
+// Measured, sustained, 4096 x 32768 x 2560: 1.70 ms, 1210 TFLOP/s (three times
+// the library's product of this size in the same run: 1.52 ms); what is over are
+// dz's way through L2, dh's fp32 sums and the ends of the launches.
 #include <algorithm>
 #include <array>
 #include <functional>
@@ -39,13 +43,27 @@ __device__ __forceinline__ float exp_of(float x) {
   return y;
 }
 
-// Common form of the h . w^T tiles: A = h rows, B = w rows, both K-major.
-template <class P>
-struct CfgCeLogits {
-  using Params = P;
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
+struct CeFwdParams {
+  int t, v, d;
+  int pieces;     // per token: one for each vocabulary tile
+  float2* piece;  // [t][pieces]: largest logit, sum of exp(logit - largest)
+  float* hit;     // [t]: the target's logit
+  const int64_t* targets;
+  uint32_t* status;
+};
+
+// A = h rows, B = w rows, both K-major.  Four epilogue warps, a row a lane: with
+// eight, half a tile's columns each, the partial sums double (8192 x 32768 x
+// 2560, sustained: 1055 against 1017 us).
+struct CfgCeFwd {
+  using Params = CeFwdParams;
+  using Tiles = StripedTiles<CfgCeFwd>;
   static constexpr bool QUANT_X = false, EARLY_TRIGGER = true;
   static constexpr int MAPS = 2;
-  static constexpr int EPI_WARPS = 4, PARTS = EPI_WARPS / 4;
+  static constexpr int EPI_WARPS = 4;
   static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
   static constexpr int A_BYTES = 128 * BK * 2;       // 16 KB
   static constexpr int B_BYTES = (BN / 2) * BK * 2;  // 16 KB
@@ -55,12 +73,14 @@ struct CfgCeLogits {
   static constexpr int E_COL0 = 0, E_COLS = 0;
   static constexpr uint32_t IDESC = idesc_bf16(256, BN, false, false);
 
-  __device__ static int rows_M(const P& p) { return p.t; }
-  __device__ static int cols_N(const P& p) { return p.v; }
-  __device__ static int k_blocks(const P& p) { return (p.d + BK - 1) / BK; }
+  __device__ static int rows_M(const Params& p) { return p.t; }
+  __device__ static int cols_N(const Params& p) { return p.v; }
+  __device__ static int k_blocks(const Params& p) { return (p.d + BK - 1) / BK; }
 
+  // Boxes of 64 rows: with few tokens a box that lies outside h costs less than
+  // a part of one (one token, 32768 x 2560: 56 against 71 us with 128 rows).
   __device__ static void load_stage(const CUtensorMap* tA, const CUtensorMap* tB, const CUtensorMap*,
-                                    const CUtensorMap*, const P&, int, uint8_t* sA, uint8_t* sB, uint8_t*, int m0,
+                                    const CUtensorMap*, const Params&, int, uint8_t* sA, uint8_t* sB, uint8_t*, int m0,
                                     int n0, int kb, uint64_t* bar) {
     tma_load_2d_pair(sA, tA, kb * BK, m0, bar);  // [64 rows][64 k] x 2
     tma_load_2d_pair(sA + 8192, tA, kb * BK, m0 + 64, bar);
@@ -68,7 +88,7 @@ struct CfgCeLogits {
     tma_load_2d_pair(sB + 8192, tB, kb * BK, n0 + 64, bar);
   }
 
-  __device__ static void mma_stage(const P&, int, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB, uint8_t*,
+  __device__ static void mma_stage(const Params&, int, uint32_t d_tmem, uint32_t, uint8_t* sA, uint8_t* sB, uint8_t*,
                                    bool first) {
     const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
 #pragma unroll
@@ -76,30 +96,13 @@ struct CfgCeLogits {
       mma_bf16_pair(d_tmem, smem_desc(a0 + kk * 32, 16, 1024, 2), smem_desc(b0 + kk * 32, 16, 1024, 2), IDESC,
                     (first && kk == 0) ? 0u : 1u);
   }
-};
 
-// ---------------------------------------------------------------------------
-// Forward
-// ---------------------------------------------------------------------------
-struct CeFwdParams {
-  int t, v, d;
-  int pieces;     // per token: two for each vocabulary tile
-  float2* piece;  // [t][pieces]: largest logit, sum of exp(logit - largest)
-  float* hit;     // [t]: the target's logit
-  const int64_t* targets;
-  uint32_t* status;
-};
-
-struct CfgCeFwd : CfgCeLogits<CeFwdParams> {
-  using Tiles = StripedTiles<CfgCeFwd>;
-
-  __device__ static void epilogue(const CeFwdParams& p, int, uint32_t t_acc, int row, int n0, int, int part,
-                                  int parts) {
+  __device__ static void epilogue(const Params& p, int, uint32_t t_acc, int row, int n0, int, int, int) {
     const bool in = row < p.t;
     const int64_t target = in ? __ldcg(p.targets + row) : -1;
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-    for (int c = part; c < BN / 32; c += parts) {
+    for (int c = 0; c < BN / 32; ++c) {
       const int col0 = n0 + c * 32;
       if (col0 >= p.v) break;  // uniform across the warp
       uint32_t r[32];
@@ -126,7 +129,7 @@ struct CfgCeFwd : CfgCeLogits<CeFwdParams> {
       sum += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
       top = best;
     }
-    if (in) p.piece[int64_t(row) * p.pieces + PARTS * (n0 / BN) + part] = make_float2(top, sum);
+    if (in) p.piece[int64_t(row) * p.pieces + n0 / BN] = make_float2(top, sum);
   }
 };
 
@@ -181,14 +184,20 @@ __global__ void __launch_bounds__(256)
 //   dw   of this piece:  A = dz MN-major (M = v), B = the scaled h MN-major, K = t
 // so that a piece costs one launch and the short tiles fill the gaps that the
 // deep ones leave.  Every operand is read in boxes of 64 x 64, which both
-// majors can use, so one tensor map each serves h, w and dz.
+// majors can use, so one tensor map each serves h, w and dz (boxes of 128 rows
+// for the K-major operands took the same time).
 //
-// dz holds exp(z - lse) - [j = target] without the row's gradient dloss: its
-// largest entries are then next to -1, where bf16 is exact for small
-// probabilities, and a row's factor stays out of that rounding.  dh multiplies
-// its fp32 sums by dloss, dw takes h already multiplied by it (one rounding to
-// bf16; one value for all rows multiplies the fp32 sums instead).
+// Where a row's factor dloss goes decides how many roundings to bf16 a product
+// carries.  From kCeWideV entries on dz holds exp(z - lse) - [j = target] alone:
+// its largest entries are next to -1, where bf16 is exact for small
+// probabilities; dh multiplies its fp32 sums by dloss, dw takes h already
+// multiplied by it (one rounding; one dloss for all rows multiplies the fp32 sums
+// instead).  With fewer entries the probabilities are near 2^-9 and above, dz's
+// largest entries are rounded anyway, and dloss goes into that same rounding.
+// Error against 64 bits over that of one rounding to bf16: dh 1.0, dw 1.3 to 1.4
+// from there on, both about 1.4 below (at 600 entries the wide way gives dw 1.7).
 // ---------------------------------------------------------------------------
+constexpr int64_t kCeWideV = 2048;
 constexpr int kCeMaxPairs = 96;
 constexpr int kCeMaxTiles = 4096;
 constexpr int kCeTileCost = 4;  // of a tile beside its blocks, in blocks: filling the pipe, the last epilogue
@@ -203,6 +212,7 @@ struct CeBwdParams {
   const float* lse;
   const float* dloss;
   int64_t dloss_stride;
+  int dz_scaled;        // dz holds dloss
   int slices, k_run;
   const float* acc;     // [slices][t up to a multiple of 32][d] fp32 sums of dh, or nullptr: dh is written directly
   int add;              // acc holds the earlier pieces' sum
@@ -381,10 +391,11 @@ struct CfgCeBwd {
     if (dz) {
       if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0) raise_status(p.status, SBL_STATUS_BAD_TARGET);
       if (live) lse = __ldcg(p.lse + row);
+      factor = live && p.dz_scaled ? __ldcg(p.dloss + row) : 1.0f;
     } else if (dw) {
       factor = p.dloss_stride == 0 ? __ldcg(p.dloss) : 1.0f;
     } else if (live) {
-      factor = __ldcg(p.dloss + row * p.dloss_stride);
+      factor = p.dz_scaled ? 1.0f : __ldcg(p.dloss + row * p.dloss_stride);
     }
     const CUtensorMap* map = dz ? &p.dz_out : dw ? &p.dw_out : &p.dh_out;
 #pragma unroll 1
@@ -404,7 +415,7 @@ struct CfgCeBwd {
           for (int e = 0; e < 32; ++e) {
             float x = exp_of(__uint_as_float(r[e]) - lse);
             if (at == e) x -= 1.0f;
-            r[e] = __float_as_uint(live ? x : 0.0f);
+            r[e] = __float_as_uint(live ? x * factor : 0.0f);
           }
         } else {
           if (!dw && p.add && in) {  // dh's last piece.  Through L2: another SM wrote it in the launch before
@@ -437,16 +448,18 @@ struct CfgCeBwd {
   }
 };
 
-// dh = dloss times the sum of its slices, in their order: 4 elements a thread.
+// dh = dloss (1 where dz holds it) times the sum of its slices, in their order: 4 elements a thread.
 __global__ void __launch_bounds__(256)
-    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t slice_n4, int64_t n4, int row_n4, const int64_t* __restrict__ targets,
-            const float* __restrict__ dloss, int64_t dloss_stride, int64_t v, int64_t ignore, uint2* __restrict__ dh) {
+    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t slice_n4, int64_t n4, int row_n4,
+            const int64_t* __restrict__ targets, const float* __restrict__ dloss, int64_t dloss_stride, int64_t v,
+            int64_t ignore, uint2* __restrict__ dh) {
   pdl_wait();
   pdl_trigger();
   const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n4) return;
   const int64_t row = i / row_n4, target = targets[row];
-  const float g = target >= 0 && target < v && target != ignore ? dloss[row * dloss_stride] : 0.0f;
+  const bool live = target >= 0 && target < v && target != ignore;
+  const float g = !live ? 0.0f : dloss != nullptr ? dloss[row * dloss_stride] : 1.0f;
   float4 a = __ldcg(acc + i);
   for (int s = 1; s < slices; ++s) {
     const float4 b = __ldcg(acc + s * slice_n4 + i);
@@ -463,6 +476,7 @@ struct CePlan {
   int64_t piece;    // vocabulary entries of a piece, a multiple of 256
   int64_t pieces;
   int slices, k_run;
+  int64_t acc_rows;  // rows of a slice of dh's sums: t up to a multiple of the 32 that a store writes
   uint64_t dz_bytes, acc_bytes, scaled_bytes;  // dz: one buffer of two (one piece: of one)
   uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + scaled_bytes; }
 };
@@ -484,7 +498,9 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   int64_t slices = std::min<int64_t>((kb0 + share - 1) / share, 32);
   c.k_run = static_cast<int>((kb0 + slices - 1) / slices);
   c.slices = static_cast<int>((kb0 + c.k_run - 1) / c.k_run);
-  c.acc_bytes = (c.pieces > 1 || c.slices > 1) ? align_up(uint64_t(c.slices) * align_up(t, 32) * uint64_t(d) * 4, 256) : 0;
+  c.acc_rows = (t + 31) / 32 * 32;
+  const uint64_t acc = uint64_t(c.slices) * uint64_t(c.acc_rows) * uint64_t(d) * 4;
+  c.acc_bytes = c.pieces > 1 || c.slices > 1 ? align_up(acc, 256) : 0;
   return c;
 }
 
@@ -535,7 +551,7 @@ bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows
 
 uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
   if (backward) return ce_plan(t, v, d).total();
-  const uint64_t pieces = CfgCeFwd::PARTS * ((uint64_t(v) + kCeTile - 1) / kCeTile);
+  const uint64_t pieces = ((uint64_t(v) + kCeTile - 1) / kCeTile);
   return align_up(uint64_t(t) * pieces * 8, 256) + align_up(uint64_t(t) * 4, 256);
 }
 
@@ -544,7 +560,7 @@ cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
   if (!rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64)) return cudaErrorInvalidValue;
   CeFwdParams p;
   p.t = static_cast<int>(a.t), p.v = static_cast<int>(a.v), p.d = static_cast<int>(a.d);
-  p.pieces = CfgCeFwd::PARTS * ((p.v + kCeTile - 1) / kCeTile);
+  p.pieces = ((p.v + kCeTile - 1) / kCeTile);
   p.piece = static_cast<float2*>(a.workspace);
   p.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + align_up(uint64_t(a.t) * p.pieces * 8, 256));
   p.targets = a.targets;
@@ -558,20 +574,23 @@ cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
 cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   const CePlan c = ce_plan(a.t, a.v, a.d);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  uint16_t* dz[2] = {reinterpret_cast<uint16_t*>(ws), reinterpret_cast<uint16_t*>(ws + (c.pieces > 1 ? c.dz_bytes : 0))};
+  uint16_t* dz[2] = {reinterpret_cast<uint16_t*>(ws),
+                     reinterpret_cast<uint16_t*>(ws + (c.pieces > 1 ? c.dz_bytes : 0))};
   ws += c.dz_bytes * (c.pieces > 1 ? 2 : 1);
   float* acc = c.acc_bytes ? reinterpret_cast<float*>(ws) : nullptr;
   ws += c.acc_bytes;
-  // dw's operand: h times dloss, or h itself where one dloss multiplies the sums
-  uint16_t* scaled = a.dloss_stride != 0 ? reinterpret_cast<uint16_t*>(ws) : nullptr;
+  // dw's operand: h times dloss, or h itself where dz holds dloss or one dloss multiplies the sums
+  const bool dz_scaled = a.dloss_stride != 0 && a.v < kCeWideV;
+  uint16_t* scaled = a.dloss_stride != 0 && !dz_scaled ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   cudaError_t e;
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd>(num_sms, &max_clusters)) != cudaSuccess) return e;
   CUtensorMap th, tw, ths, dh_out, acc_out;
-  if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * ((a.t + 31) / 32 * 32), a.d * 4, 32,
-                                        32, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * c.acc_rows,
+                                        a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  if (!rows_map(&dh_out, a.dh, a.d, a.t, a.d, 32) || !rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
+  if (!rows_map(&dh_out, a.dh, a.d, a.t, a.d, 32) || !rows_map(&th, a.h, a.d, a.t, a.d, 64) ||
+      !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
       !rows_map(&ths, scaled ? scaled : a.h, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
@@ -581,7 +600,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     p.zv = static_cast<int>(wide(i + 1)), p.zfirst = (i + 1) * c.piece;
     p.vv = static_cast<int>(wide(i)), p.vfirst = i * c.piece;
     p.targets = a.targets, p.v_all = a.v, p.ignore = a.ignore_index;
-    p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride;
+    p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride, p.dz_scaled = dz_scaled;
     p.k_run = c.k_run;
     p.slices = ((p.vv + 63) / 64 + c.k_run - 1) / c.k_run;
     p.acc = acc;
@@ -613,8 +632,9 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   if (c.slices > 1) {
     const int64_t n4 = a.t * a.d / 4;
     return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
-                      reinterpret_cast<const float4*>(acc), c.slices, (a.t + 31) / 32 * 32 * a.d / 4, n4, static_cast<int>(a.d / 4), a.targets, a.dloss,
-                      a.dloss_stride, a.v, a.ignore_index, reinterpret_cast<uint2*>(a.dh));
+                      reinterpret_cast<const float4*>(acc), c.slices, c.acc_rows * a.d / 4, n4,
+                      static_cast<int>(a.d / 4), a.targets, dz_scaled ? nullptr : a.dloss, a.dloss_stride, a.v, a.ignore_index,
+                      reinterpret_cast<uint2*>(a.dh));
   }
   return cudaSuccess;
 }

@@ -193,8 +193,8 @@ sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* t
     return code(cudaMemsetAsync(dw, 0, size_t(v) * size_t(d) * 2, s));
   }
   if (!h || !w || !targets || !lse || !dloss || !dh || !workspace) return SBL_ERR_INVALID_ARG;
-  if (!all_aligned16({h, w, dh}) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(workspace, 256) ||
-      !aligned(status_dev, 4))
+  if (!all_aligned16({h, w, dh}) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dloss, 4) ||
+      !aligned(workspace, 256) || !aligned(status_dev, 4))
     return SBL_ERR_ALIGN;
   if ((st = current_device(&sms)) != SBL_OK) return st;
   CeArgs a = {};

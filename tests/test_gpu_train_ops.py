@@ -88,9 +88,30 @@ def test_norm_row_lengths_and_types(k, xt, rt):
         check_norm(norm_all(x, res, w), x, res, w)
 
 
+@pytest.mark.parametrize("k", [8, 64, 264, 768, 1024, 1032, 2048, 2560, 4096, 4104, 5128, 6912, 8200, 12288, 16384])
+@pytest.mark.parametrize("xt,rt", NORM_TYPES)
+def test_norm_rows_walked_by_resident_blocks(k, xt, rt):
+    """More than two rows an SM: blocks walk rows (other warps a row, other vectors a lane), one row or several a block."""
+    t = 1801 if k <= 1032 else 701
+    x = randn(t, k, seed=k, dtype=xt)
+    res = None if rt is None else randn(t, k, seed=k + 1, std=2.0, dtype=rt)
+    w = randn(k, seed=3, std=0.2, mean=1.0, dtype=BF if k % 16 else F32)
+    x[5] = 0
+    if res is not None:
+        res[5] = 0
+    check_norm(norm_all(x, res, w), x, res, w)
+    if k in (1024, 16384):
+        check_norm(norm_all(x, res), x, res, None)
+
+
 def test_norm_many_rows():
     x, res, w = randn(4099, 2560, seed=1), randn(4099, 2560, seed=2, dtype=BF), randn(2560, seed=3, dtype=BF)
     check_norm(norm_all(x, res, w), x, res, w)
+    # the stream in place, with the next row's loads under way
+    stream = res.clone()
+    xn = torch.empty_like(res)
+    sbl.rmsnorm_forward(x, 4099, 2560, EPS, residual=stream, weight=w, h_out=stream, xn_out=xn)
+    assert same_bits(stream, (x + res.float()).to(BF))
 
 
 def test_norm_zero_rows_and_extreme_magnitudes():
@@ -236,6 +257,21 @@ def test_norm_backward_row_lengths_and_types(k, ht, dt):
         dres = randn(t, k, seed=30, dtype=ht) if with_res else None
         out, rstd = norm_bwd(h, dys, w, dres)
         check_norm_bwd(out, rstd, h, dys, w, dres)
+
+
+@pytest.mark.parametrize("k", [8, 256, 264, 1000, 1032, 2048, 2560, 4104, 6912, 12288, 16384])
+@pytest.mark.parametrize("ht,dt", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
+def test_norm_backward_rings_of_many_rows(k, ht, dt):
+    """Several rows a group and several groups a block, rings of every depth that the sizes give."""
+    t = 5003 if k <= 1032 else 1801 if k <= 4104 else 601
+    count = 1 + k // 8 % 3
+    h = randn(t, k, seed=k, std=2.0, dtype=ht)
+    dys = [randn(t, k, seed=20 + i, dtype=dt) for i in range(count)]
+    w, dres = randn(k, seed=3, std=0.2, mean=1.0, dtype=BF), randn(t, k, seed=30, dtype=ht)
+    out, rstd = norm_bwd(h, dys, w, dres)
+    check_norm_bwd(out, rstd, h, dys, w, dres)
+    out, rstd = norm_bwd(h, dys[:1], None, None, rstd=rstd)
+    check_norm_bwd(out, rstd, h, dys[:1], None, None)
 
 
 def test_norm_backward_many_rows_in_place_and_repeatable():
@@ -629,7 +665,7 @@ def test_linear_ce_backward(t, v, d):
     assert same_bits(again[0], dh) and same_bits(again[1], dw)
 
 
-@pytest.mark.parametrize("t,v,d", [(4100, 9001, 64), (9000, 8193, 264), (9000, 12001, 64)])
+@pytest.mark.parametrize("t,v,d", [(4100, 9001, 64), (9000, 8193, 264), (9000, 12001, 64), (300, 150001, 64)])
 def test_linear_ce_backward_in_pieces(t, v, d):
     h, w, y = ce_inputs(t, v, d, 5)
     loss, lse = ce_forward(h, w, y)
@@ -638,6 +674,17 @@ def test_linear_ce_backward_in_pieces(t, v, d):
     launched = sbl.launch_count()
     dh, dw = ce_backward(h, w, y, lse, dloss)
     assert sbl.launch_count() - launched >= 3  # dz of the first piece, two pieces at least
+    check_ce_bwd(dh, dw, h, w, y, lse, dloss)
+
+
+def test_linear_ce_backward_of_many_tiles():
+    """More output tiles than the launch's table of tiles holds: they are striped over the SMs instead."""
+    t, v, d = 256, 40000, 8192
+    h, w, y = ce_inputs(t, v, d, 7, std=0.01)
+    loss, lse = ce_forward(h, w, y)
+    check_ce(loss, lse, h, w, y)
+    dloss = randn(t, seed=9, std=0.3, mean=1.0)
+    dh, dw = ce_backward(h, w, y, lse, dloss)
     check_ce_bwd(dh, dw, h, w, y, lse, dloss)
 
 
