@@ -367,36 +367,59 @@ enum {
  *   xn   = RN_bf16(RN_fp32(RN_fp32(h rstd) weight)); weight NULL: 1
  *   xscale, xq = the codes that sbl_quantize_activations gives for xn, bit for bit
  *   xhat = RN_bf16(xq xscale / 127), the dW operand of SBL_DW_QUANT_X
- * x, residual: [t, k]; weight: [k].  Outputs, each may be NULL, one at least
- * is wanted: h_out [t, k] (the stream's type; without a residual x's type),
- * xn_out and xhat_out bf16 [t, k], xq_out int8 [t, k], xscale_out fp32 [t],
- * rstd_out fp32 [t].  h_out may be `residual`.  k: a multiple of 8 up to SBL_NORM_MAX_K (of 64 when
+ * h_out may be `residual`.  k: a multiple of 8 up to SBL_NORM_MAX_K (of 64 when
  * the codes are to enter sbl_forward_quantized); eps: 1e-12 to 1.  A row of
  * zeros gives xn = 0, xscale = 1e-5, xq = 0.  A non-finite h or xn raises
  * SBL_STATUS_NONFINITE_X; the other rows are not touched by it.  t == 0 is a
  * no-op.  Errors: SBL_ERR_SHAPE (t, k), SBL_ERR_INVALID_ARG (eps, an unknown
  * flag, no x, no output), SBL_ERR_ALIGN, SBL_ERR_DEVICE, SBL_ERR_CUDA. */
-sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* weight, int64_t t, int64_t k,
-                               double eps, uint32_t flags, void* h_out, void* xn_out, void* xhat_out, int8_t* xq_out,
-                               float* xscale_out, float* rstd_out, uint32_t* status_dev, sbl_stream_t stream);
+typedef struct sbl_rmsnorm_args {
+  const void* x;        /* [t, k] */
+  const void* residual; /* [t, k] in the stream's type, or NULL */
+  const void* weight;   /* [k], or NULL */
+  int64_t t, k;
+  double eps;
+  /* outputs, each may be NULL, one at least is wanted */
+  void* h_out;          /* [t, k], the stream's type; without a residual x's type */
+  void* xn_out;         /* bf16 [t, k] */
+  void* xhat_out;       /* bf16 [t, k] */
+  int8_t* xq_out;       /* [t, k] */
+  float* xscale_out;    /* [t] */
+  float* rstd_out;      /* [t] */
+  uint32_t* status_dev;
+  uint32_t flags;       /* SBL_NORM_X_F32, _STREAM_F32, _W_F32 */
+  uint32_t reserved;    /* 0 */
+} sbl_rmsnorm_args;
+sbl_status sbl_rmsnorm_forward(const sbl_rmsnorm_args* args, sbl_stream_t stream);
 
-/* Backward of the above, straight through the quantiser.  dys: `dy_count`
- * (1 to 3) pointers to gradients [t, k] of xn, which are added (the dX of the
- * products that share the input: q, k and v; gate and up); dres [t, k] (NULL:
- * zero) the gradient that reaches h along the residual stream.
+/* Backward of the above, straight through the quantiser.
  *   g   = sum dys,  n = h rstd
- *   dh  = dres + rstd (weight g - n mean_k(weight g n))   [t, k], the stream's type
- *   dx  = RN_bf16 of the same value, optional (the dy that sbl_backward of the
- *         linear in front takes when the stream is fp32)
- *   dw  = sum_t g n   fp32 [k], optional
+ *   dh  = dres + rstd (weight g - n mean_k(weight g n))
+ *   dx  = RN_bf16 of the same value
+ *   dw  = sum_t g n
  * dh is the gradient of x and of residual alike.  h is the forward's h_out (or
  * its x, without a residual) in the stream's type.  dh may be dres.  dw needs
  * `workspace`, sbl_rmsnorm_backward_workspace_bytes(t, k) bytes, 16-byte
  * aligned; its sum has a fixed order.  rstd needs 4-byte alignment only.
  * t == 0: dw = 0.  Errors as the forward's. */
-sbl_status sbl_rmsnorm_backward(const void* h, const float* rstd, const void* weight, const void* const* dys,
-                                int32_t dy_count, const void* dres, int64_t t, int64_t k, uint32_t flags, void* dh,
-                                void* dx, float* dw, void* workspace, sbl_stream_t stream);
+typedef struct sbl_rmsnorm_backward_args {
+  const void* h;        /* [t, k] in the stream's type */
+  const float* rstd;    /* [t], the forward's rstd_out */
+  const void* weight;   /* [k], or NULL */
+  const void* dys[3];   /* dy_count gradients [t, k] of xn, which are added: the dX of the
+                           products that share the input (q, k and v; gate and up) */
+  const void* dres;     /* [t, k] in the stream's type: the gradient that reaches h along the
+                           residual stream; NULL: zero */
+  int64_t t, k;
+  void* dh;             /* [t, k], the stream's type */
+  void* dx;             /* bf16 [t, k], or NULL: the dy that sbl_backward of the linear in front
+                           takes when the stream is fp32 */
+  float* dw;            /* [k], or NULL */
+  void* workspace;
+  uint32_t flags;       /* SBL_NORM_STREAM_F32, _W_F32, _DY_F32 */
+  int32_t dy_count;     /* 1 to 3 */
+} sbl_rmsnorm_backward_args;
+sbl_status sbl_rmsnorm_backward(const sbl_rmsnorm_backward_args* args, sbl_stream_t stream);
 size_t sbl_rmsnorm_backward_workspace_bytes(int64_t t, int64_t k);
 
 /* Flags of sbl_adamw_tensor.flags. */
@@ -457,24 +480,30 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
 
 /* Softmax cross entropy of a linear head, without its logits in memory:
  *   z = h w^T,  lse_i = log sum_j exp z_ij,  loss_i = lse_i - z_i,target_i
- * h: bf16 [t, d]; w: bf16 [v, d]; targets: int64 [t], `ignore_index` for rows
- * without loss (loss 0; lse is still written).  loss, lse: fp32 [t].  d: a
- * multiple of 8 up to 131072; v >= 1 and t up to 2^22.  A target outside
- * [0, v) that is not ignore_index gives loss NaN and raises
- * SBL_STATUS_BAD_TARGET; a bounded wait that ran out raises
- * SBL_STATUS_TIMEOUT, here and in the backward pass.  targets, loss, lse and dloss need only their
- * elements' own alignment.  `workspace`: sbl_linear_ce_workspace_bytes(t, v, d,
- * 0) bytes, 256-byte aligned.  t == 0 is a no-op.  Errors: SBL_ERR_SHAPE (t, v,
- * d), SBL_ERR_INVALID_ARG (a NULL pointer), SBL_ERR_ALIGN, SBL_ERR_DEVICE,
- * SBL_ERR_CUDA. */
-sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* targets, int64_t t, int64_t v, int64_t d,
-                                 int64_t ignore_index, float* loss, float* lse, void* workspace, uint32_t* status_dev,
-                                 sbl_stream_t stream);
+ * d: a multiple of 8 up to 131072; v >= 1, v and t up to 2^22.  Rows whose target
+ * is ignore_index have loss 0 (lse is still written).  A target outside [0, v)
+ * that is not ignore_index gives loss NaN and raises SBL_STATUS_BAD_TARGET; a
+ * bounded wait that ran out raises SBL_STATUS_TIMEOUT, here and in the backward
+ * pass.  targets, loss, lse and dloss need only their elements' own alignment.
+ * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 0) bytes, 256-byte aligned.
+ * t == 0 is a no-op.  Errors: SBL_ERR_SHAPE (t, v, d), SBL_ERR_INVALID_ARG (a NULL
+ * pointer), SBL_ERR_ALIGN, SBL_ERR_DEVICE, SBL_ERR_CUDA. */
+typedef struct sbl_linear_ce_args {
+  const void* h;          /* bf16 [t, d] */
+  const void* w;          /* bf16 [v, d] */
+  const int64_t* targets; /* [t] */
+  int64_t t, v, d, ignore_index;
+  float* loss;            /* [t] */
+  float* lse;             /* [t] */
+  void* workspace;
+  uint32_t* status_dev;
+} sbl_linear_ce_args;
+sbl_status sbl_linear_ce_forward(const sbl_linear_ce_args* args, sbl_stream_t stream);
 
-/* Its backward pass from the forward's lse.  dloss: fp32, the gradient of each
- * row's loss, dloss[i * dloss_stride] (stride 0: one value for all rows).
+/* Its backward pass from the forward's lse; dloss is the gradient of each row's
+ * loss, dloss[i * dloss_stride] (stride 0: one value for all rows).
  *   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]), 0 for ignored rows and rows with a bad target
- *   dh = dz w  bf16 [t, d],   dw = dz^T h  bf16 [v, d]
+ *   dh = dz w,   dw = dz^T h
  * The logits are computed again, a piece of the vocabulary at a time.  For the
  * two products, which accumulate in fp32, dz is rounded to bf16 below 2048
  * entries; from there on exp(z - lse) - [j = target] is, and for dw also
@@ -483,10 +512,20 @@ sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* ta
  * aligned.  Rows without loss give dh = 0 whatever their lse and dloss hold.
  * t == 0: dw = 0.  Errors: as the forward, plus SBL_ERR_INVALID_ARG for a
  * dloss_stride other than 0 and 1. */
-sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,
-                                  const float* dloss, int64_t dloss_stride, int64_t t, int64_t v, int64_t d,
-                                  int64_t ignore_index, void* dh, void* dw, void* workspace, uint32_t* status_dev,
-                                  sbl_stream_t stream);
+typedef struct sbl_linear_ce_backward_args {
+  const void* h;          /* bf16 [t, d] */
+  const void* w;          /* bf16 [v, d] */
+  const int64_t* targets; /* [t] */
+  const float* lse;       /* [t] */
+  const float* dloss;     /* [t], or one value */
+  int64_t dloss_stride;   /* 1, or 0 */
+  int64_t t, v, d, ignore_index;
+  void* dh;               /* bf16 [t, d] */
+  void* dw;               /* bf16 [v, d] */
+  void* workspace;
+  uint32_t* status_dev;
+} sbl_linear_ce_backward_args;
+sbl_status sbl_linear_ce_backward(const sbl_linear_ce_backward_args* args, sbl_stream_t stream);
 /* 0 for sizes the calls refuse. */
 size_t sbl_linear_ce_workspace_bytes(int64_t t, int64_t v, int64_t d, int32_t backward);
 

@@ -555,24 +555,27 @@ uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
   return align_up(uint64_t(t) * pieces * 8, 256) + align_up(uint64_t(t) * 4, 256);
 }
 
-cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_linear_ce(const sbl_linear_ce_args& a, int num_sms, cudaStream_t s) {
+  const uint16_t *h = static_cast<const uint16_t*>(a.h), *w = static_cast<const uint16_t*>(a.w);
   CUtensorMap th, tw;
-  if (!rows_map(&th, a.h, a.d, a.t, a.d, 64) || !rows_map(&tw, a.w, a.d, a.v, a.d, 64)) return cudaErrorInvalidValue;
+  if (!rows_map(&th, h, a.d, a.t, a.d, 64) || !rows_map(&tw, w, a.d, a.v, a.d, 64)) return cudaErrorInvalidValue;
   CeFwdParams p;
   p.t = static_cast<int>(a.t), p.v = static_cast<int>(a.v), p.d = static_cast<int>(a.d);
   p.pieces = ((p.v + kCeTile - 1) / kCeTile);
   p.piece = static_cast<float2*>(a.workspace);
   p.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + align_up(uint64_t(a.t) * p.pieces * 8, 256));
   p.targets = a.targets;
-  p.status = a.status;
+  p.status = a.status_dev;
   const cudaError_t e = launch_pair<CfgCeFwd>(th, tw, tw, p, p.t, p.v, num_sms, s, true);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_ce_join, dim3((p.t + 7) / 8), dim3(256), 0, s, p.piece, p.pieces, p.hit, a.targets, p.t, a.v,
-                    a.ignore_index, a.loss, a.lse, a.status);
+                    a.ignore_index, a.loss, a.lse, a.status_dev);
 }
 
-cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_sms, cudaStream_t s) {
   const CePlan c = ce_plan(a.t, a.v, a.d);
+  const uint16_t *h = static_cast<const uint16_t*>(a.h), *w = static_cast<const uint16_t*>(a.w);
+  uint16_t *dh = static_cast<uint16_t*>(a.dh), *dw = static_cast<uint16_t*>(a.dw);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   uint16_t* dz[2] = {reinterpret_cast<uint16_t*>(ws),
                      reinterpret_cast<uint16_t*>(ws + (c.pieces > 1 ? c.dz_bytes : 0))};
@@ -589,9 +592,9 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
   if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * c.acc_rows,
                                         a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  if (!rows_map(&dh_out, a.dh, a.d, a.t, a.d, 32) || !rows_map(&th, a.h, a.d, a.t, a.d, 64) ||
-      !rows_map(&tw, a.w, a.d, a.v, a.d, 64) ||
-      !rows_map(&ths, scaled ? scaled : a.h, a.d, a.t, a.d, 64))
+  if (!rows_map(&dh_out, dh, a.d, a.t, a.d, 32) || !rows_map(&th, h, a.d, a.t, a.d, 64) ||
+      !rows_map(&tw, w, a.d, a.v, a.d, 64) ||
+      !rows_map(&ths, scaled ? scaled : h, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
   for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
@@ -606,13 +609,13 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
-    p.h = a.h, p.scaled = i < 0 ? scaled : nullptr;
-    p.status = a.status;
+    p.h = h, p.scaled = i < 0 ? scaled : nullptr;
+    p.status = a.status_dev;
     CUtensorMap tz = th;
     p.dz_out = p.dw_out = p.acc_out = p.dh_out = dh_out;
     if (p.zv > 0 && !rows_map(&p.dz_out, dz[(i + 1) & 1], p.zv, a.t, c.piece, 32)) return cudaErrorInvalidValue;
     if (p.vv > 0 && (!rows_map(&tz, dz[i & 1], p.vv, a.t, c.piece, 64) ||
-                     !rows_map(&p.dw_out, a.dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
+                     !rows_map(&p.dw_out, dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
       return cudaErrorInvalidValue;
     if (acc != nullptr) p.acc_out = acc_out;
     const int n_dh = CfgCeBwd::tiles_dh(p), n_dw = CfgCeBwd::tiles_dw(p), n_dz = CfgCeBwd::tiles_dz(p);
@@ -634,7 +637,7 @@ cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s) {
     return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
                       reinterpret_cast<const float4*>(acc), c.slices, c.acc_rows * a.d / 4, n4,
                       static_cast<int>(a.d / 4), a.targets, dz_scaled ? nullptr : a.dloss, a.dloss_stride, a.v, a.ignore_index,
-                      reinterpret_cast<uint2*>(a.dh));
+                      reinterpret_cast<uint2*>(dh));
   }
   return cudaSuccess;
 }

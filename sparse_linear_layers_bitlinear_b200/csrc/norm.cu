@@ -800,15 +800,16 @@ cudaError_t pick_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_rmsnorm(const sbl_rmsnorm_args& a, int num_sms, cudaStream_t s) {
   NormParams p;
   p.x = a.x, p.res = a.residual, p.w = a.weight;
   p.t = a.t, p.nvec = static_cast<int>(a.k / 8);
   p.inv_k = 1.0 / static_cast<double>(a.k), p.eps = a.eps;
   p.w_f32 = (a.flags & SBL_NORM_W_F32) != 0u;
-  p.h = a.h;
-  p.xn = static_cast<uint4*>(a.xn), p.xhat = static_cast<uint4*>(a.xhat), p.xq = reinterpret_cast<uint2*>(a.xq);
-  p.xscale = a.xscale, p.rstd = a.rstd, p.status = a.status;
+  p.h = a.h_out;
+  p.xn = static_cast<uint4*>(a.xn_out), p.xhat = static_cast<uint4*>(a.xhat_out);
+  p.xq = reinterpret_cast<uint2*>(a.xq_out);
+  p.xscale = a.xscale_out, p.rstd = a.rstd_out, p.status = a.status_dev;
   const bool xf = (a.flags & SBL_NORM_X_F32) != 0u, rf = (a.flags & SBL_NORM_STREAM_F32) != 0u;
   if (a.residual == nullptr)
     return xf ? pick_norm<true, kNoRes>(p, num_sms, s) : pick_norm<false, kNoRes>(p, num_sms, s);
@@ -818,7 +819,7 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s) {
 
 int64_t rmsnorm_bwd_max_blocks(int64_t t) { return t < kNormBwdMaxBlocks ? t : kNormBwdMaxBlocks; }
 
-cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_rmsnorm_bwd(const sbl_rmsnorm_backward_args& a, int num_sms, cudaStream_t s) {
   NormBwdParams p;
   p.h = a.h, p.rstd = a.rstd, p.w = a.weight;
   for (int i = 0; i < 3; ++i) p.dy[i] = i < a.dy_count ? a.dys[i] : nullptr;

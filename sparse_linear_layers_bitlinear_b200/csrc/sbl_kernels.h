@@ -130,35 +130,11 @@ cudaError_t launch_bf16_backward_dual(bool out_f32, const uint16_t* dy, const ui
                                       const uint8_t* dw_mask, int mask_m, uint32_t* status, int num_sms,
                                       cudaStream_t s, bool* done);
 
-// RMS norm (norm.cu): arguments as sbl_rmsnorm_forward / _backward.
-struct NormArgs {
-  const void *x, *residual, *weight;
-  int64_t t, k;
-  double eps;
-  uint32_t flags;
-  void *h, *xn, *xhat;
-  int8_t* xq;
-  float *xscale, *rstd;
-  uint32_t* status;
-};
-cudaError_t launch_rmsnorm(const NormArgs& a, int num_sms, cudaStream_t s);
-
-struct NormBwdArgs {
-  const void* h;
-  const float* rstd;
-  const void* weight;
-  const void* const* dys;
-  int dy_count;
-  const void* dres;
-  int64_t t, k;
-  uint32_t flags;
-  void *dh, *dx;
-  float* dw;
-  void* workspace;
-};
+// RMS norm (norm.cu), the arguments checked.
+cudaError_t launch_rmsnorm(const sbl_rmsnorm_args& a, int num_sms, cudaStream_t s);
 constexpr int kNormBwdMaxBlocks = 256;  // rows of partial sums the workspace may hold
 int64_t rmsnorm_bwd_max_blocks(int64_t t);
-cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_rmsnorm_bwd(const sbl_rmsnorm_backward_args& a, int num_sms, cudaStream_t s);
 
 // AdamW (adamw.cu): the tensors of one launch (count up to kAdamMaxTensors,
 // none of them empty).
@@ -166,21 +142,10 @@ constexpr int kAdamMaxTensors = 128;
 cudaError_t launch_adamw(const sbl_adamw_tensor* tensors, int count, const sbl_adamw_params& params, uint32_t* status,
                          cudaStream_t s);
 
-// Linear cross entropy (linear_ce.cu).
-struct CeArgs {
-  const uint16_t *h, *w;
-  const int64_t* targets;
-  int64_t t, v, d, ignore_index;
-  float *loss, *lse;  // backward: lse is read
-  const float* dloss;
-  int64_t dloss_stride;
-  uint16_t *dh, *dw;
-  void* workspace;
-  uint32_t* status;
-};
+// Linear cross entropy (linear_ce.cu), the arguments checked.
 uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward);
-cudaError_t launch_linear_ce(const CeArgs& a, int num_sms, cudaStream_t s);
-cudaError_t launch_linear_ce_bwd(const CeArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_ce(const sbl_linear_ce_args& a, int num_sms, cudaStream_t s);
+cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_sms, cudaStream_t s);
 
 cudaError_t launch_selftest_wait(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
 cudaError_t launch_chain_floor(int blocks, cudaStream_t s);

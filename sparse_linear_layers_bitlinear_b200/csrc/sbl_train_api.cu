@@ -41,23 +41,21 @@ bool factor(double x) { return std::isfinite(x) && x >= 0.0; }
 
 extern "C" {
 
-sbl_status sbl_rmsnorm_forward(const void* x, const void* residual, const void* weight, int64_t t, int64_t k,
-                               double eps, uint32_t flags, void* h_out, void* xn_out, void* xhat_out, int8_t* xq_out,
-                               float* xscale_out, float* rstd_out, uint32_t* status_dev, sbl_stream_t stream) {
-  if ((flags & ~kNormFwdFlags) != 0u) return SBL_ERR_INVALID_ARG;
-  if (!norm_shape(t, k)) return SBL_ERR_SHAPE;
-  if (!(eps >= 1e-12 && eps <= 1.0)) return SBL_ERR_INVALID_ARG;
-  if (t == 0) return SBL_OK;
-  if (x == nullptr) return SBL_ERR_INVALID_ARG;
-  if (!h_out && !xn_out && !xhat_out && !xq_out && !xscale_out && !rstd_out) return SBL_ERR_INVALID_ARG;
-  if (!all_aligned16({x, residual, weight, h_out, xn_out, xhat_out, xq_out, xscale_out, rstd_out}) ||
-      !aligned(status_dev, 4))
+sbl_status sbl_rmsnorm_forward(const sbl_rmsnorm_args* args, sbl_stream_t stream) {
+  if (args == nullptr) return SBL_ERR_INVALID_ARG;
+  const sbl_rmsnorm_args& a = *args;
+  if ((a.flags & ~kNormFwdFlags) != 0u || a.reserved != 0u) return SBL_ERR_INVALID_ARG;
+  if (!norm_shape(a.t, a.k)) return SBL_ERR_SHAPE;
+  if (!(a.eps >= 1e-12 && a.eps <= 1.0)) return SBL_ERR_INVALID_ARG;
+  if (a.t == 0) return SBL_OK;
+  if (a.x == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!a.h_out && !a.xn_out && !a.xhat_out && !a.xq_out && !a.xscale_out && !a.rstd_out) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({a.x, a.residual, a.weight, a.h_out, a.xn_out, a.xhat_out, a.xq_out, a.xscale_out, a.rstd_out}) ||
+      !aligned(a.status_dev, 4))
     return SBL_ERR_ALIGN;
   int sms = 0;
   const sbl_status st = current_device(&sms);
   if (st != SBL_OK) return st;
-  const NormArgs a{x, residual, weight, t, k, eps, flags, h_out, xn_out, xhat_out, xq_out, xscale_out, rstd_out,
-                   status_dev};
   return code(launch_rmsnorm(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -66,30 +64,29 @@ size_t sbl_rmsnorm_backward_workspace_bytes(int64_t t, int64_t k) {
   return size_t(rmsnorm_bwd_max_blocks(t)) * size_t(k) * 4;
 }
 
-sbl_status sbl_rmsnorm_backward(const void* h, const float* rstd, const void* weight, const void* const* dys,
-                                int32_t dy_count, const void* dres, int64_t t, int64_t k, uint32_t flags, void* dh,
-                                void* dx, float* dw, void* workspace, sbl_stream_t stream) {
-  if ((flags & ~kNormBwdFlags) != 0u || dy_count < 1 || dy_count > 3) return SBL_ERR_INVALID_ARG;
-  if (!norm_shape(t, k)) return SBL_ERR_SHAPE;
-  if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
+sbl_status sbl_rmsnorm_backward(const sbl_rmsnorm_backward_args* args, sbl_stream_t stream) {
+  if (args == nullptr) return SBL_ERR_INVALID_ARG;
+  const sbl_rmsnorm_backward_args& a = *args;
+  if ((a.flags & ~kNormBwdFlags) != 0u || a.dy_count < 1 || a.dy_count > 3) return SBL_ERR_INVALID_ARG;
+  if (!norm_shape(a.t, a.k)) return SBL_ERR_SHAPE;
+  if (!aligned(a.dw, 16)) return SBL_ERR_ALIGN;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
-  if (t == 0) {
-    if (dw == nullptr) return SBL_OK;
+  if (a.t == 0) {
+    if (a.dw == nullptr) return SBL_OK;
     const sbl_status st = current_device(&sms);
     if (st != SBL_OK) return st;
-    return code(cudaMemsetAsync(dw, 0, size_t(k) * 4, s));
+    return code(cudaMemsetAsync(a.dw, 0, size_t(a.k) * 4, s));
   }
-  if (h == nullptr || rstd == nullptr || dys == nullptr || dh == nullptr) return SBL_ERR_INVALID_ARG;
-  for (int i = 0; i < dy_count; ++i) {
-    if (dys[i] == nullptr) return SBL_ERR_INVALID_ARG;
-    if (!aligned(dys[i], 16)) return SBL_ERR_ALIGN;
+  if (a.h == nullptr || a.rstd == nullptr || a.dh == nullptr) return SBL_ERR_INVALID_ARG;
+  for (int i = 0; i < a.dy_count; ++i) {
+    if (a.dys[i] == nullptr) return SBL_ERR_INVALID_ARG;
+    if (!aligned(a.dys[i], 16)) return SBL_ERR_ALIGN;
   }
-  if (dw != nullptr && workspace == nullptr) return SBL_ERR_INVALID_ARG;
-  if (!all_aligned16({h, weight, dres, dh, dx, workspace}) || !aligned(rstd, 4)) return SBL_ERR_ALIGN;
+  if (a.dw != nullptr && a.workspace == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({a.h, a.weight, a.dres, a.dh, a.dx, a.workspace}) || !aligned(a.rstd, 4)) return SBL_ERR_ALIGN;
   const sbl_status st = current_device(&sms);
   if (st != SBL_OK) return st;
-  const NormBwdArgs a{h, rstd, weight, dys, dy_count, dres, t, k, flags, dh, dx, dw, workspace};
   return code(launch_rmsnorm_bwd(a, sms, s));
 }
 
@@ -158,51 +155,40 @@ size_t sbl_linear_ce_workspace_bytes(int64_t t, int64_t v, int64_t d, int32_t ba
   return static_cast<size_t>(linear_ce_workspace(t, v, d, backward != 0));
 }
 
-sbl_status sbl_linear_ce_forward(const void* h, const void* w, const int64_t* targets, int64_t t, int64_t v, int64_t d,
-                                 int64_t ignore_index, float* loss, float* lse, void* workspace, uint32_t* status_dev,
-                                 sbl_stream_t stream) {
-  if (!ce_shape(t, v, d)) return SBL_ERR_SHAPE;
-  if (t == 0) return SBL_OK;
-  if (!h || !w || !targets || !loss || !lse || !workspace) return SBL_ERR_INVALID_ARG;
-  if (!all_aligned16({h, w}) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
-      !aligned(workspace, 256) || !aligned(status_dev, 4))
+sbl_status sbl_linear_ce_forward(const sbl_linear_ce_args* args, sbl_stream_t stream) {
+  if (args == nullptr) return SBL_ERR_INVALID_ARG;
+  const sbl_linear_ce_args& a = *args;
+  if (!ce_shape(a.t, a.v, a.d)) return SBL_ERR_SHAPE;
+  if (a.t == 0) return SBL_OK;
+  if (!a.h || !a.w || !a.targets || !a.loss || !a.lse || !a.workspace) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({a.h, a.w}) || !aligned(a.targets, 8) || !aligned(a.loss, 4) || !aligned(a.lse, 4) ||
+      !aligned(a.workspace, 256) || !aligned(a.status_dev, 4))
     return SBL_ERR_ALIGN;
   int sms = 0;
   const sbl_status st = current_device(&sms);
   if (st != SBL_OK) return st;
-  CeArgs a = {};
-  a.h = static_cast<const uint16_t*>(h), a.w = static_cast<const uint16_t*>(w), a.targets = targets;
-  a.t = t, a.v = v, a.d = d, a.ignore_index = ignore_index;
-  a.loss = loss, a.lse = lse, a.workspace = workspace, a.status = status_dev;
   return code(launch_linear_ce(a, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-sbl_status sbl_linear_ce_backward(const void* h, const void* w, const int64_t* targets, const float* lse,
-                                  const float* dloss, int64_t dloss_stride, int64_t t, int64_t v, int64_t d,
-                                  int64_t ignore_index, void* dh, void* dw, void* workspace, uint32_t* status_dev,
-                                  sbl_stream_t stream) {
-  if (!ce_shape(t, v, d)) return SBL_ERR_SHAPE;
-  if (dloss_stride != 0 && dloss_stride != 1) return SBL_ERR_INVALID_ARG;
-  if (dw == nullptr) return SBL_ERR_INVALID_ARG;
-  if (!aligned(dw, 16)) return SBL_ERR_ALIGN;
+sbl_status sbl_linear_ce_backward(const sbl_linear_ce_backward_args* args, sbl_stream_t stream) {
+  if (args == nullptr) return SBL_ERR_INVALID_ARG;
+  const sbl_linear_ce_backward_args& a = *args;
+  if (!ce_shape(a.t, a.v, a.d)) return SBL_ERR_SHAPE;
+  if (a.dloss_stride != 0 && a.dloss_stride != 1) return SBL_ERR_INVALID_ARG;
+  if (a.dw == nullptr) return SBL_ERR_INVALID_ARG;
+  if (!aligned(a.dw, 16)) return SBL_ERR_ALIGN;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int sms = 0;
   sbl_status st;
-  if (t == 0) {  // no rows: dh is empty and dw = 0
+  if (a.t == 0) {  // no rows: dh is empty and dw = 0
     if ((st = current_device(&sms)) != SBL_OK) return st;
-    return code(cudaMemsetAsync(dw, 0, size_t(v) * size_t(d) * 2, s));
+    return code(cudaMemsetAsync(a.dw, 0, size_t(a.v) * size_t(a.d) * 2, s));
   }
-  if (!h || !w || !targets || !lse || !dloss || !dh || !workspace) return SBL_ERR_INVALID_ARG;
-  if (!all_aligned16({h, w, dh}) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(dloss, 4) ||
-      !aligned(workspace, 256) || !aligned(status_dev, 4))
+  if (!a.h || !a.w || !a.targets || !a.lse || !a.dloss || !a.dh || !a.workspace) return SBL_ERR_INVALID_ARG;
+  if (!all_aligned16({a.h, a.w, a.dh}) || !aligned(a.targets, 8) || !aligned(a.lse, 4) || !aligned(a.dloss, 4) ||
+      !aligned(a.workspace, 256) || !aligned(a.status_dev, 4))
     return SBL_ERR_ALIGN;
   if ((st = current_device(&sms)) != SBL_OK) return st;
-  CeArgs a = {};
-  a.h = static_cast<const uint16_t*>(h), a.w = static_cast<const uint16_t*>(w), a.targets = targets;
-  a.t = t, a.v = v, a.d = d, a.ignore_index = ignore_index;
-  a.lse = const_cast<float*>(lse), a.dloss = dloss, a.dloss_stride = dloss_stride;
-  a.dh = static_cast<uint16_t*>(dh), a.dw = static_cast<uint16_t*>(dw);
-  a.workspace = workspace, a.status = status_dev;
   try {
     return code(launch_linear_ce_bwd(a, sms, s));
   } catch (const std::bad_alloc&) {

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -89,10 +90,13 @@ class sbl_adamw_tensor(ctypes.Structure):
         ("numel", ctypes.c_int64), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
-class sbl_adamw_params(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
-        ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p), ("step_dev", ctypes.c_void_p),
-        ("grad_scale_dev", ctypes.c_void_p)]
+# The argument structs of the entry points that take one, as packed bytes: a
+# call then costs the host less than a ctypes argument for every field.
+_RMSNORM_ARGS = struct.Struct("=3Q2qd7Q2I")
+_RMSNORM_BACKWARD_ARGS = struct.Struct("=7Q2q4QIi")
+_ADAMW_PARAMS = struct.Struct("=5dq3Q")
+_LINEAR_CE_ARGS = struct.Struct("=3Q4q4Q")
+_LINEAR_CE_BACKWARD_ARGS = struct.Struct("=5Q5q4Q")
 
 
 # Every entry point of include/sbl.h with its ctypes signature.
@@ -122,12 +126,12 @@ SIGNATURES = {
     "sbl_weight_abs_sum": (_I32, [_LP, _P, _P, _P]),
     "sbl_prepare_weights_from_sum": (_I32, [_LP, _P, _P, _I64, _P]),
     "sbl_forward_quantized": (_I32, [_LP, _P, _P, _I64, _P, _P, _P]),
-    "sbl_rmsnorm_forward": (_I32, [_P, _P, _P, _I64, _I64, ctypes.c_double, _U32, _P, _P, _P, _P, _P, _P, _P, _P]),
-    "sbl_rmsnorm_backward": (_I32, [_P, _P, _P, _P, _I32, _P, _I64, _I64, _U32, _P, _P, _P, _P, _P]),
+    "sbl_rmsnorm_forward": (_I32, [ctypes.c_char_p, _P]),
+    "sbl_rmsnorm_backward": (_I32, [ctypes.c_char_p, _P]),
     "sbl_rmsnorm_backward_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
-    "sbl_adamw_step": (_I32, [_P, _I32, _P, _P, _P]),
-    "sbl_linear_ce_forward": (_I32, [_P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
-    "sbl_linear_ce_backward": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "sbl_adamw_step": (_I32, [_P, _I32, ctypes.c_char_p, _P, _P]),
+    "sbl_linear_ce_forward": (_I32, [ctypes.c_char_p, _P]),
+    "sbl_linear_ce_backward": (_I32, [ctypes.c_char_p, _P]),
     "sbl_linear_ce_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I32]),
 }
 
@@ -389,9 +393,10 @@ class _Types:
         self.float = (torch.bfloat16, torch.float32)
         self.i8, self.u8, self.i32, self.i64 = (torch.int8,), (torch.uint8,), (torch.int32,), (torch.int64,)
         self.code8 = (torch.float8_e4m3fn, torch.uint8)
-        self.current_device = torch.cuda.current_device
-        # the raw handle of torch's current stream: a call's cost on the host is most of a small call's time
-        self.raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+        # the current device and the raw handle of its current stream without the objects around them: a call's
+        # cost on the host is most of a small call's time
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _torch_types() -> _Types:
@@ -412,9 +417,9 @@ def _device(T: _Types, what: str, name: str, t) -> int:
 
 
 def _addr(what: str, name: str, t, dtypes, numel: int, dev: int):
-    """The address of tensor `t` after its checks; None stays None (the library refuses a NULL it needs)."""
+    """The address of tensor `t` after its checks; 0 for None (the library refuses a NULL it needs)."""
     if t is None:
-        return None
+        return 0
     if t.dtype in dtypes and t.get_device() == dev and t.is_contiguous() and t.numel() == numel:
         return t.data_ptr()
     if t.dtype not in dtypes:
@@ -428,7 +433,7 @@ def _addr(what: str, name: str, t, dtypes, numel: int, dev: int):
 
 def _room(T: _Types, what: str, t, nbytes: int, dev: int):
     """The address of a uint8 workspace of `nbytes` or more."""
-    return None if t is None else _addr(what, "workspace", t, T.u8, max(t.numel(), nbytes), dev)
+    return 0 if t is None else _addr(what, "workspace", t, T.u8, max(t.numel(), nbytes), dev)
 
 
 def _raw_stream(T: _Types, stream, dev: int):
@@ -450,13 +455,12 @@ def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h
     stream_type = T.f32 if (x if residual is None else residual).dtype in T.f32 else T.bf16
     flags = ((SBL_NORM_X_F32 if x.dtype in T.f32 else 0) | (SBL_NORM_STREAM_F32 if stream_type is T.f32 else 0)
              | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
-    code = lib().sbl_rmsnorm_forward(
-        xp, _addr(me, "residual", residual, stream_type, n, dev), _addr(me, "weight", weight, T.float, k, dev),
-        t, k, eps, flags, _addr(me, "h_out", h_out, stream_type, n, dev),
-        _addr(me, "xn_out", xn_out, T.bf16, n, dev), _addr(me, "xhat_out", xhat_out, T.bf16, n, dev),
-        _addr(me, "xq_out", xq_out, T.i8, n, dev), _addr(me, "xscale_out", xscale_out, T.f32, t, dev),
-        _addr(me, "rstd_out", rstd_out, T.f32, t, dev), _addr(me, "status", status, T.i32, 1, dev),
-        _raw_stream(T, stream, dev))
+    code = lib().sbl_rmsnorm_forward(_RMSNORM_ARGS.pack(
+        xp, _addr(me, "residual", residual, stream_type, n, dev), _addr(me, "weight", weight, T.float, k, dev), t, k, eps,
+        _addr(me, "h_out", h_out, stream_type, n, dev), _addr(me, "xn_out", xn_out, T.bf16, n, dev),
+        _addr(me, "xhat_out", xhat_out, T.bf16, n, dev), _addr(me, "xq_out", xq_out, T.i8, n, dev),
+        _addr(me, "xscale_out", xscale_out, T.f32, t, dev), _addr(me, "rstd_out", rstd_out, T.f32, t, dev),
+        _addr(me, "status", status, T.i32, 1, dev), flags, 0), _raw_stream(T, stream, dev))
     if code:
         raise SblError(code, me)
 
@@ -483,12 +487,13 @@ def rmsnorm_backward(h, rstd, dys, t: int, k: int, dh, weight=None, dres=None, d
              | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
     if dy_type[0] not in T.float:
         dy_type = T.float
-    dyp = (_P * 3)(*[_addr(me, "dys", d, dy_type, n, dev) for d in dys])
-    ws = _room(T, me, workspace, rmsnorm_backward_workspace_bytes(t, k), dev) if dw is not None else None
-    code = lib().sbl_rmsnorm_backward(
-        hp, _addr(me, "rstd", rstd, T.f32, t, dev), _addr(me, "weight", weight, T.float, k, dev), dyp, len(dys),
-        _addr(me, "dres", dres, stream_type, n, dev), t, k, flags, _addr(me, "dh", dh, stream_type, n, dev),
-        _addr(me, "dx", dx, T.bf16, n, dev), _addr(me, "dw", dw, T.f32, k, dev), ws, _raw_stream(T, stream, dev))
+    dyp = [_addr(me, "dys", d, dy_type, n, dev) for d in dys] + [0] * (3 - len(dys))
+    ws = _room(T, me, workspace, rmsnorm_backward_workspace_bytes(t, k), dev) if dw is not None else 0
+    code = lib().sbl_rmsnorm_backward(_RMSNORM_BACKWARD_ARGS.pack(
+        hp, _addr(me, "rstd", rstd, T.f32, t, dev), _addr(me, "weight", weight, T.float, k, dev), *dyp,
+        _addr(me, "dres", dres, stream_type, n, dev), t, k, _addr(me, "dh", dh, stream_type, n, dev),
+        _addr(me, "dx", dx, T.bf16, n, dev), _addr(me, "dw", dw, T.f32, k, dev), ws, flags, len(dys)),
+        _raw_stream(T, stream, dev))
     if code:
         raise SblError(code, me)
 
@@ -567,10 +572,10 @@ def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, 
     dev = tensors.device
     if dev != T.current_device():
         raise SblError(SBL_ERR_DEVICE, f"{me}: the tensors are not on the current CUDA device")
-    params = sbl_adamw_params(lr, beta1, beta2, eps, weight_decay, step, _addr(me, "lr_dev", lr_dev, T.f32, 1, dev),
-                              _addr(me, "step_dev", step_dev, T.i64, 1, dev),
-                              _addr(me, "grad_scale_dev", grad_scale_dev, T.f32, 1, dev))
-    code = lib().sbl_adamw_step(tensors.array, tensors.count, ctypes.byref(params),
+    params = _ADAMW_PARAMS.pack(lr, beta1, beta2, eps, weight_decay, step, _addr(me, "lr_dev", lr_dev, T.f32, 1, dev),
+                                _addr(me, "step_dev", step_dev, T.i64, 1, dev),
+                                _addr(me, "grad_scale_dev", grad_scale_dev, T.f32, 1, dev))
+    code = lib().sbl_adamw_step(tensors.array, tensors.count, params,
                                 _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
     if code:
         raise SblError(code, me)
@@ -587,11 +592,11 @@ def linear_ce_forward(h, w, targets, t: int, v: int, d: int, loss, lse, workspac
     targets: int64 [t], workspace: uint8, linear_ce_workspace_bytes(t, v, d)."""
     T, me = _torch_types(), "sbl_linear_ce_forward"
     dev = _device(T, me, "h", h)
-    code = lib().sbl_linear_ce_forward(
+    code = lib().sbl_linear_ce_forward(_LINEAR_CE_ARGS.pack(
         _addr(me, "h", h, T.bf16, t * d, dev), _addr(me, "w", w, T.bf16, v * d, dev),
         _addr(me, "targets", targets, T.i64, t, dev), t, v, d, ignore_index, _addr(me, "loss", loss, T.f32, t, dev),
         _addr(me, "lse", lse, T.f32, t, dev), _room(T, me, workspace, linear_ce_workspace_bytes(t, v, d), dev),
-        _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
+        _addr(me, "status", status, T.i32, 1, dev)), _raw_stream(T, stream, dev))
     if code:
         raise SblError(code, me)
 
@@ -604,13 +609,13 @@ def linear_ce_backward(h, w, targets, lse, dloss, t: int, v: int, d: int, dh, dw
     T, me = _torch_types(), "sbl_linear_ce_backward"
     dev = _device(T, me, "h", h)
     one = dloss is not None and dloss.numel() == 1
-    code = lib().sbl_linear_ce_backward(
+    code = lib().sbl_linear_ce_backward(_LINEAR_CE_BACKWARD_ARGS.pack(
         _addr(me, "h", h, T.bf16, t * d, dev), _addr(me, "w", w, T.bf16, v * d, dev),
         _addr(me, "targets", targets, T.i64, t, dev), _addr(me, "lse", lse, T.f32, t, dev),
         _addr(me, "dloss", dloss, T.f32, 1 if one else t, dev), 0 if one else 1, t, v, d, ignore_index,
         _addr(me, "dh", dh, T.bf16, t * d, dev), _addr(me, "dw", dw, T.bf16, v * d, dev),
         _room(T, me, workspace, linear_ce_workspace_bytes(t, v, d, True), dev),
-        _addr(me, "status", status, T.i32, 1, dev), _raw_stream(T, stream, dev))
+        _addr(me, "status", status, T.i32, 1, dev)), _raw_stream(T, stream, dev))
     if code:
         raise SblError(code, me)
 
