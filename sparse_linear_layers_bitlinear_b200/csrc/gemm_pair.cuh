@@ -290,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads<Cfg>(),
       const uint32_t t_acc = tmem_base + ab * Cfg::ACC_COLS + (uint32_t(quarter * 32) << 16);
       if constexpr (PairOut<Cfg>::bytes > 0)
         Cfg::epilogue(p, t.prob, t_acc, m0 + quarter * 32, n0, lane,
-                      smO + (warp - 2) * (PairOut<Cfg>::bytes / Cfg::EPI_WARPS));
+                      smO + (warp - 2) * (PairOut<Cfg>::bytes / Cfg::EPI_WARPS), part, parts);
       else
         Cfg::epilogue(p, t.prob, t_acc, m0 + quarter * 32 + lane, n0, lane, part, parts);
       tc_fence_before();

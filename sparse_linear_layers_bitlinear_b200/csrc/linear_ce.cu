@@ -57,7 +57,7 @@ struct CeFwdParams {
 
 // A = h rows, B = w rows, both K-major.  Four epilogue warps, a row a lane: with
 // eight, half a tile's columns each, the partial sums double (8192 x 32768 x
-// 2560, sustained: 1055 against 1017 us).
+// 2560, sustained: 1055 against 1017 us; 63 x 4099 x 512: 9.9 against 10.0).
 struct CfgCeFwd {
   using Params = CeFwdParams;
   using Tiles = StripedTiles<CfgCeFwd>;
@@ -225,12 +225,16 @@ struct CeBwdParams {
   uint16_t sched[kCeMaxTiles];
 };
 
+// EPI epilogue warps: 4, or 8 with half of a tile's columns each where no pair of
+// SMs has more than one tile and the epilogue's own time counts (63 x 4099 x 512:
+// 17.1 against 18.4 us; 4 keep a stage more of operands).
+template <int EPI>
 struct CfgCeBwd {
   using Params = CeBwdParams;
   static constexpr bool QUANT_X = false, EARLY_TRIGGER = true;
   static constexpr int MAPS = 4;
-  static constexpr int EPI_WARPS = 4;
-  static constexpr int BN = kCeTile, BK = 64, STAGES = 6;
+  static constexpr int EPI_WARPS = EPI;
+  static constexpr int BN = kCeTile, BK = 64, STAGES = EPI > 4 ? 5 : 6;  // the boxes take the sixth's place
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = (BN / 2) * BK * 2;
   static constexpr int E_BYTES = 0;
@@ -364,8 +368,11 @@ struct CfgCeBwd {
     }
   }
 
-  // row0: the warp's first row, one row a lane.
-  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row0, int n0, int lane, uint8_t* box) {
+  // row0: the warp's first row, one row a lane; of the tile's boxes side by side
+  // every `parts`-th from `part` on.
+  __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row0, int n0, int lane, uint8_t* box,
+                                  int part, int parts) {
+    int turn = 0;
     const bool dz = prob == kDz, dw = prob == kDw;
     const int rows = dw ? p.vv : p.t, cols = dz ? p.zv : p.d;
     if (row0 >= rows) return;
@@ -375,13 +382,13 @@ struct CfgCeBwd {
     if (!dz && !dw && p.acc != nullptr && !p.last) {  // dh's fp32 sums: stored by the first piece, then added to
       const int y = (prob - kDh) * up(p.t, 32) * 32 + row0;
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = part; c < BN / 32; c += parts, turn ^= 4096) {
         uint32_t r[32];
         __syncwarp();
         tmem_load_32x32b_x32(t_acc + c * 32, r);
         tmem_load_wait();
         if (n0 + c * 32 >= cols) break;
-        put(&p.acc_out, r, box + (c & 1) * 4096, lane, n0 + c * 32, y, p.add);
+        put(&p.acc_out, r, box + turn, lane, n0 + c * 32, y, p.add);
       }
       return;
     }
@@ -389,7 +396,8 @@ struct CfgCeBwd {
     const bool live = good(p, target);
     float factor = 0.0f, lse = 0.0f;
     if (dz) {
-      if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0) raise_status(p.status, SBL_STATUS_BAD_TARGET);
+      if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0 && part == 0)
+        raise_status(p.status, SBL_STATUS_BAD_TARGET);
       if (live) lse = __ldcg(p.lse + row);
       factor = live && p.dz_scaled ? __ldcg(p.dloss + row) : 1.0f;
     } else if (dw) {
@@ -399,7 +407,7 @@ struct CfgCeBwd {
     }
     const CUtensorMap* map = dz ? &p.dz_out : dw ? &p.dw_out : &p.dh_out;
 #pragma unroll 1
-    for (int c = 0; c < BN / 64; ++c) {
+    for (int c = part; c < BN / 64; c += parts, turn ^= 4096) {
       const int col0 = n0 + c * 64;
       if (col0 >= cols) break;  // uniform across the warp
       uint32_t word[32];
@@ -443,7 +451,7 @@ struct CfgCeBwd {
           word[16 * h + e] = *reinterpret_cast<const uint32_t*>(&h2);
         }
       }
-      put(map, word, box + (c & 1) * 4096, lane, col0, row0, false);
+      put(map, word, box + turn, lane, col0, row0, false);
     }
   }
 };
@@ -551,9 +559,24 @@ bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows
 
 uint64_t linear_ce_workspace(int64_t t, int64_t v, int64_t d, bool backward) {
   if (backward) return ce_plan(t, v, d).total();
-  const uint64_t pieces = ((uint64_t(v) + kCeTile - 1) / kCeTile);
+  const uint64_t pieces = (uint64_t(v) + kCeTile - 1) / kCeTile;
   return align_up(uint64_t(t) * pieces * 8, 256) + align_up(uint64_t(t) * 4, 256);
 }
+
+namespace {
+
+template <int EPI>
+cudaError_t launch_ce_tiles(const CUtensorMap& th, const CUtensorMap& tw, const CUtensorMap& tz, const CUtensorMap& ths,
+                            const CeBwdParams& p, int pairs, int num_sms, cudaStream_t s) {
+  using Cfg = CfgCeBwd<EPI>;
+  int max_clusters = 0;
+  const cudaError_t e = pair_setup<Cfg>(num_sms, &max_clusters);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_gemm_pair<Cfg>, dim3(2 * pairs), dim3(pair_threads<Cfg>()), pair_smem_bytes<Cfg>(), s, th, tw, tz,
+                    ths, p);
+}
+
+}  // namespace
 
 cudaError_t launch_linear_ce(const sbl_linear_ce_args& a, int num_sms, cudaStream_t s) {
   const uint16_t *h = static_cast<const uint16_t*>(a.h), *w = static_cast<const uint16_t*>(a.w);
@@ -561,7 +584,7 @@ cudaError_t launch_linear_ce(const sbl_linear_ce_args& a, int num_sms, cudaStrea
   if (!rows_map(&th, h, a.d, a.t, a.d, 64) || !rows_map(&tw, w, a.d, a.v, a.d, 64)) return cudaErrorInvalidValue;
   CeFwdParams p;
   p.t = static_cast<int>(a.t), p.v = static_cast<int>(a.v), p.d = static_cast<int>(a.d);
-  p.pieces = ((p.v + kCeTile - 1) / kCeTile);
+  p.pieces = (p.v + kCeTile - 1) / kCeTile;
   p.piece = static_cast<float2*>(a.workspace);
   p.hit = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + align_up(uint64_t(a.t) * p.pieces * 8, 256));
   p.targets = a.targets;
@@ -587,7 +610,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
   uint16_t* scaled = a.dloss_stride != 0 && !dz_scaled ? reinterpret_cast<uint16_t*>(ws) : nullptr;
   cudaError_t e;
   int max_clusters = 0;
-  if ((e = pair_setup<CfgCeBwd>(num_sms, &max_clusters)) != cudaSuccess) return e;
+  if ((e = pair_setup<CfgCeBwd<4>>(num_sms, &max_clusters)) != cudaSuccess) return e;
   CUtensorMap th, tw, ths, dh_out, acc_out;
   if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * c.acc_rows,
                                         a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -618,7 +641,8 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
                      !rows_map(&p.dw_out, dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
       return cudaErrorInvalidValue;
     if (acc != nullptr) p.acc_out = acc_out;
-    const int n_dh = CfgCeBwd::tiles_dh(p), n_dw = CfgCeBwd::tiles_dw(p), n_dz = CfgCeBwd::tiles_dz(p);
+    using Cfg = CfgCeBwd<4>;
+    const int n_dh = Cfg::tiles_dh(p), n_dw = Cfg::tiles_dw(p), n_dz = Cfg::tiles_dz(p);
     const int64_t tiles = int64_t(n_dh) + n_dw + n_dz;
     const int pairs = static_cast<int>(std::min<int64_t>({tiles, max_clusters, kCeMaxPairs}));
     p.tabled = tiles <= kCeMaxTiles;
@@ -628,16 +652,16 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
       std::copy(sch.off.begin(), sch.off.end(), p.sched_off);
       std::copy(sch.ids.begin(), sch.ids.end(), p.sched);
     }
-    e = launch_pdl(k_gemm_pair<CfgCeBwd>, dim3(2 * pairs), dim3(pair_threads<CfgCeBwd>()), pair_smem_bytes<CfgCeBwd>(),
-                   s, th, tw, tz, ths, p);
+    e = tiles <= pairs ? launch_ce_tiles<8>(th, tw, tz, ths, p, pairs, num_sms, s)
+                       : launch_ce_tiles<4>(th, tw, tz, ths, p, pairs, num_sms, s);
     if (e != cudaSuccess) return e;
   }
   if (c.slices > 1) {
     const int64_t n4 = a.t * a.d / 4;
     return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
                       reinterpret_cast<const float4*>(acc), c.slices, c.acc_rows * a.d / 4, n4,
-                      static_cast<int>(a.d / 4), a.targets, dz_scaled ? nullptr : a.dloss, a.dloss_stride, a.v, a.ignore_index,
-                      reinterpret_cast<uint2*>(dh));
+                      static_cast<int>(a.d / 4), a.targets, dz_scaled ? nullptr : a.dloss, a.dloss_stride, a.v,
+                      a.ignore_index, reinterpret_cast<uint2*>(dh));
   }
   return cudaSuccess;
 }

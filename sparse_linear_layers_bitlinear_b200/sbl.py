@@ -456,8 +456,8 @@ def rmsnorm_forward(x, t: int, k: int, eps: float, residual=None, weight=None, h
     flags = ((SBL_NORM_X_F32 if x.dtype in T.f32 else 0) | (SBL_NORM_STREAM_F32 if stream_type is T.f32 else 0)
              | (SBL_NORM_W_F32 if weight is not None and weight.dtype in T.f32 else 0))
     code = lib().sbl_rmsnorm_forward(_RMSNORM_ARGS.pack(
-        xp, _addr(me, "residual", residual, stream_type, n, dev), _addr(me, "weight", weight, T.float, k, dev), t, k, eps,
-        _addr(me, "h_out", h_out, stream_type, n, dev), _addr(me, "xn_out", xn_out, T.bf16, n, dev),
+        xp, _addr(me, "residual", residual, stream_type, n, dev), _addr(me, "weight", weight, T.float, k, dev),
+        t, k, eps, _addr(me, "h_out", h_out, stream_type, n, dev), _addr(me, "xn_out", xn_out, T.bf16, n, dev),
         _addr(me, "xhat_out", xhat_out, T.bf16, n, dev), _addr(me, "xq_out", xq_out, T.i8, n, dev),
         _addr(me, "xscale_out", xscale_out, T.f32, t, dev), _addr(me, "rstd_out", rstd_out, T.f32, t, dev),
         _addr(me, "status", status, T.i32, 1, dev), flags, 0), _raw_stream(T, stream, dev))
