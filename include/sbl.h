@@ -507,9 +507,11 @@ sbl_status sbl_linear_ce_forward(const sbl_linear_ce_args* args, sbl_stream_t st
  * The logits are computed again, a piece of the vocabulary at a time.  For the
  * two products, which accumulate in fp32, dz is rounded to bf16 below 2048
  * entries; from there on exp(z - lse) - [j = target] is, and for dw also
- * dloss_i h_i (with stride 0: dloss multiplies the sums in either range).
+ * dloss_i h_i (with stride 0: dloss multiplies the sums in either range).  lse is
+ * fp32: a probability's relative error grows as |lse| 2^-24.
  * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 1) bytes, 256-byte
- * aligned.  Rows without loss give dh = 0 whatever their lse and dloss hold.
+ * aligned.  Rows without loss give dh = 0 and add nothing to dw,
+ * whatever their h, lse and dloss hold.
  * t == 0: dw = 0.  Errors: as the forward, plus SBL_ERR_INVALID_ARG for a
  * dloss_stride other than 0 and 1. */
 typedef struct sbl_linear_ce_backward_args {

@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kCeTile = 256;
 
-// exp(x) to about 2^-22 (relative), results below 2^-126 zero.
+// exp(x), relative error about (2 + |x|) 2^-23, results below 2^-126 zero.
 __device__ __forceinline__ float exp_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
@@ -218,7 +218,8 @@ struct CeBwdParams {
   int add;              // acc holds the earlier pieces' sum
   int last;             // with one slice: write dh instead of acc
   const uint16_t* h;
-  uint16_t* scaled;     // the first launch: where h times dloss goes (or nullptr)
+  uint16_t* scaled;     // the first launch: where dw's operand goes (else nullptr)
+  int row_factor;       // dw's operand is h times dloss, else h
   uint32_t* status;
   int tabled;           // tiles from the table, else striped
   uint16_t sched_off[kCeMaxPairs + 1];
@@ -270,7 +271,7 @@ struct CfgCeBwd {
     }
   };
 
-  // Maps: h, w, this piece's dz, h times dloss.
+  // Maps: h, w, this piece's dz, dw's operand of h.
   __device__ static void load_stage(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tz,
                                     const CUtensorMap* ths, const Params& p, int prob, uint8_t* sA, uint8_t* sB,
                                     uint8_t*, int m0, int n0, int kb, uint64_t* bar) {
@@ -317,15 +318,18 @@ struct CfgCeBwd {
     return target >= 0 && target < p.v_all && target != p.ignore;
   }
 
-  // The first launch: h times each row's dloss for dw, zero for rows without
-  // loss, a row a warp, while the first tiles' products run.
+  // The first launch: dw's operand, h (or h times each row's dloss) with zeros in
+  // the rows without loss, whose h may hold anything: zero times a NaN would reach
+  // dw.  A row a warp, while the first tiles' products run (4096 x 2560: nothing
+  // beside 32768 entries, 2 us of 54 beside 1000; loads of several rows at once
+  // took no less).
   __device__ static void prologue(const Params& p, int warp, int warps, int lane) {
     if (p.scaled == nullptr) return;
     pdl_wait();  // h, targets and dloss may come from the kernel before
     const int vecs = p.d / 8;
     for (int row = warp; row < p.t; row += warps) {
       const bool live = good(p, __ldcg(p.targets + row));
-      const float g = live ? __ldcg(p.dloss + row) : 0.0f;
+      const float g = live && p.row_factor ? __ldcg(p.dloss + row) : 1.0f;
       const uint4* src = reinterpret_cast<const uint4*>(p.h) + int64_t(row) * vecs;
       uint4* dst = reinterpret_cast<uint4*>(p.scaled) + int64_t(row) * vecs;
 #pragma unroll 4
@@ -513,18 +517,22 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
 }
 
 // The tiles of one launch over the pairs, deepest first, each to the pair with
-// the least work so far.  Cached per shape.
+// the least work so far, written into p.  Cached per shape.
 struct CeSchedule {
   std::vector<uint16_t> off, ids;
 };
 
-const CeSchedule& ce_schedule(int n_dh, int k_dh, int n_dw, int k_dw, int n_dz, int k_dz, int npairs) {
+void ce_schedule(int n_dh, int k_dh, int n_dw, int k_dw, int n_dz, int k_dz, int npairs, CeBwdParams& p) {
   static std::mutex mu;
   static std::map<std::array<int, 7>, CeSchedule> cache;
   std::lock_guard<std::mutex> lock(mu);
   const std::array<int, 7> key = {n_dh, k_dh, n_dw, k_dw, n_dz, k_dz, npairs};
+  const auto use = [&p](const CeSchedule& sch) {
+    std::copy(sch.off.begin(), sch.off.end(), p.sched_off);
+    std::copy(sch.ids.begin(), sch.ids.end(), p.sched);
+  };
   const auto it = cache.find(key);
-  if (it != cache.end()) return it->second;
+  if (it != cache.end()) return use(it->second);
   struct Kind {
     int first, n, depth;
   };
@@ -547,7 +555,9 @@ const CeSchedule& ce_schedule(int n_dh, int k_dh, int n_dw, int k_dw, int n_dz, 
     sch.ids.insert(sch.ids.end(), ids.begin(), ids.end());
     sch.off.push_back(static_cast<uint16_t>(sch.ids.size()));
   }
-  return cache.emplace(key, std::move(sch)).first->second;
+  use(sch);
+  if (cache.size() >= 512) cache.clear();  // 8 KB each at most
+  cache.emplace(key, std::move(sch));
 }
 
 bool rows_map(CUtensorMap* map, const uint16_t* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
@@ -605,9 +615,8 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
   ws += c.dz_bytes * (c.pieces > 1 ? 2 : 1);
   float* acc = c.acc_bytes ? reinterpret_cast<float*>(ws) : nullptr;
   ws += c.acc_bytes;
-  // dw's operand: h times dloss, or h itself where dz holds dloss or one dloss multiplies the sums
   const bool dz_scaled = a.dloss_stride != 0 && a.v < kCeWideV;
-  uint16_t* scaled = a.dloss_stride != 0 && !dz_scaled ? reinterpret_cast<uint16_t*>(ws) : nullptr;
+  uint16_t* scaled = reinterpret_cast<uint16_t*>(ws);  // dw's operand
   cudaError_t e;
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd<4>>(num_sms, &max_clusters)) != cudaSuccess) return e;
@@ -617,7 +626,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     return cudaErrorInvalidValue;
   if (!rows_map(&dh_out, dh, a.d, a.t, a.d, 32) || !rows_map(&th, h, a.d, a.t, a.d, 64) ||
       !rows_map(&tw, w, a.d, a.v, a.d, 64) ||
-      !rows_map(&ths, scaled ? scaled : h, a.d, a.t, a.d, 64))
+      !rows_map(&ths, scaled, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
   for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
@@ -633,6 +642,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
     p.h = h, p.scaled = i < 0 ? scaled : nullptr;
+    p.row_factor = a.dloss_stride != 0 && !dz_scaled;  // else dz holds dloss, or it multiplies the sums
     p.status = a.status_dev;
     CUtensorMap tz = th;
     p.dz_out = p.dw_out = p.acc_out = p.dh_out = dh_out;
@@ -644,14 +654,12 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     using Cfg = CfgCeBwd<4>;
     const int n_dh = Cfg::tiles_dh(p), n_dw = Cfg::tiles_dw(p), n_dz = Cfg::tiles_dz(p);
     const int64_t tiles = int64_t(n_dh) + n_dw + n_dz;
-    const int pairs = static_cast<int>(std::min<int64_t>({tiles, max_clusters, kCeMaxPairs}));
+    // the first launch has a warp for each row to copy too, if need be on pairs without a tile
+    const int64_t busy = i < 0 ? std::max<int64_t>(tiles, (a.t + 7) / 8) : tiles;
+    const int pairs = static_cast<int>(std::min<int64_t>({busy, max_clusters, kCeMaxPairs}));
     p.tabled = tiles <= kCeMaxTiles;
-    if (p.tabled) {
-      const CeSchedule& sch = ce_schedule(n_dh, std::min(c.k_run, (p.vv + 63) / 64), n_dw, (p.t + 63) / 64, n_dz,
-                                          (p.d + 63) / 64, pairs);
-      std::copy(sch.off.begin(), sch.off.end(), p.sched_off);
-      std::copy(sch.ids.begin(), sch.ids.end(), p.sched);
-    }
+    if (p.tabled)
+      ce_schedule(n_dh, std::min(c.k_run, (p.vv + 63) / 64), n_dw, (p.t + 63) / 64, n_dz, (p.d + 63) / 64, pairs, p);
     e = tiles <= pairs ? launch_ce_tiles<8>(th, tw, tz, ths, p, pairs, num_sms, s)
                        : launch_ce_tiles<4>(th, tw, tz, ths, p, pairs, num_sms, s);
     if (e != cudaSuccess) return e;

@@ -346,9 +346,10 @@ cudaError_t launch_norm(const NormParams& p, int warps, int num_sms, cudaStream_
     // one wave of blocks, each with its share of the rows
     int fit = 0;
     cudaError_t e = cudaSuccess;
-    if (smem > 40 * 1024)  // with the static arrays past the 48 KB that need no asking
+    if (smem > 40 * 1024)  // with the static arrays past the 48 KB that need no asking; the same for every size:
+                           // another thread's call may come between this one's asking and its launch
       e = cudaFuncSetAttribute(k_rmsnorm<XF32, RES, R, ONE_WARP, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem));
+                               SBL_NORM_MAX_K * 4);
     if (e == cudaSuccess)
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, k_rmsnorm<XF32, RES, R, ONE_WARP, FEW>, threads, smem);
     if (e != cudaSuccess) return e;
@@ -432,6 +433,7 @@ struct NormBwdParams {
 };
 
 constexpr int kNormBwdThreads = 512, kNormBwdRuns = 5;  // of a block; runs of 256 elements a warp at most
+constexpr int kNormBwdSmem = 224 * 1024;                // dynamic shared memory of a block at most
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* smem, const void* gmem) {
@@ -746,8 +748,9 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float4* __restrict__ part
 
 template <bool HF32, bool DF32, int R, bool RING>
 cudaError_t launch_norm_bwd(const NormBwdParams& p, int blocks, size_t smem, cudaStream_t s) {
+  // the same for every size: another thread's call may come between this and the launch
   const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd<HF32, DF32, R, RING>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kNormBwdSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_rmsnorm_bwd<HF32, DF32, R, RING>, dim3(blocks), dim3(32 * p.warps * p.groups), smem, s, p);
 }
@@ -768,7 +771,7 @@ cudaError_t pick_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t 
   const int r = up(p.nvec, 32 * p.warps);
   p.words = r * ((HF32 ? 2 : 1) * 2 + (DF32 ? 2 : 1) * p.ndy);
   const size_t weight = p.w != nullptr ? size_t(p.warps) * r * 1024 : 0;  // fp32, behind the ring
-  const size_t room = 224 * 1024 - weight;
+  const size_t room = kNormBwdSmem - weight;
   const size_t one = size_t(p.words) * 16 * 32 * p.warps;
   const auto depth = [&](int groups) { return static_cast<int>(std::min<size_t>(room / (one * groups), 3)); };
   const int most = static_cast<int>(std::min<int64_t>({std::max(14 / p.warps, 1), (p.t + num_sms - 1) / num_sms}));

@@ -3,7 +3,6 @@
 #include <algorithm>
 #include <cmath>
 #include <functional>
-#include <new>
 #include <vector>
 
 #include "sbl_kernels.h"
@@ -145,7 +144,7 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
       if (!launch()) return SBL_ERR_CUDA;
     }
     return SBL_OK;
-  } catch (const std::bad_alloc&) {
+  } catch (...) {
     return SBL_ERR_INVALID_ARG;  // a count the host cannot hold
   }
 }
@@ -191,7 +190,7 @@ sbl_status sbl_linear_ce_backward(const sbl_linear_ce_backward_args* args, sbl_s
   if ((st = current_device(&sms)) != SBL_OK) return st;
   try {
     return code(launch_linear_ce_bwd(a, sms, s));
-  } catch (const std::bad_alloc&) {
+  } catch (...) {
     return SBL_ERR_CUDA;  // no host memory for the tile schedule
   }
 }

@@ -705,8 +705,30 @@ def test_linear_ce_backward_rows_without_loss():
     assert st.item() == sbl.SBL_STATUS_BAD_TARGET and not dh.any() and not dw.any()
     e = torch.empty(0, 64, dtype=BF, device="cuda")
     dw.fill_(3)
-    sbl.linear_ce_backward(e, w, y[:0], lse[:0], dloss[:0], 0, 333, 64, e, dw, torch.empty(0, dtype=torch.uint8, device="cuda"))
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    sbl.linear_ce_backward(e, w, y[:0], lse[:0], dloss[:0], 0, 333, 64, e, dw, none)
     assert not dw.any()
+
+
+@pytest.mark.parametrize("one", [False, True], ids=["each", "one"])
+@pytest.mark.parametrize("t,v,d", [(90, 333, 64), (5, 9, 8), (700, 2500, 136), (4100, 9001, 64)])
+def test_linear_ce_backward_of_padding_that_holds_anything(t, v, d, one):
+    """Rows without loss may hold NaN and infinities: they reach no gradient."""
+    h, w, y = ce_inputs(t, v, d, 11)  # every seventh row is ignored
+    y[1], y[2] = v, -1                # and two targets are bad
+    dead = (y < 0) | (y >= v)
+    assert dead.sum() >= 3
+    loss, lse = ce_forward(h, w, y)
+    dloss = randn(1 if one else t, seed=9, std=0.3, mean=1.0)
+    dh, dw = ce_backward(h, w, y, lse, dloss)
+    check_ce_bwd(dh, dw, h, w, y, lse, dloss)
+    dirty = h.clone()
+    dirty[dead] = float("nan")
+    dirty[0] = float("inf") if dead[0] else dirty[0]
+    loss2, lse2 = ce_forward(dirty, w, y)
+    assert same_bits(loss2[~dead], loss[~dead]) and same_bits(lse2[~dead], lse[~dead])
+    got = ce_backward(dirty, w, y, lse2, dloss)
+    assert same_bits(got[0], dh) and same_bits(got[1], dw)
 
 
 def test_linear_ce_gradient_against_differences():
