@@ -187,23 +187,26 @@ __global__ void __launch_bounds__(256)
 // majors can use, so one tensor map each serves h, w and dz (boxes of 128 rows
 // for the K-major operands took the same time).
 //
-// Where a row's factor dloss goes decides how many roundings to bf16 a product
-// carries.  From kCeWideV entries on dz holds exp(z - lse) - [j = target] alone:
-// its largest entries are next to -1, where bf16 is exact for small
-// probabilities; dh multiplies its fp32 sums by dloss, dw takes h already
+// How dz becomes bf16, and where a row's factor dloss goes, decides how many
+// roundings a product carries.  From kCeWideV entries on dz holds exp(z - lse) -
+// [j = target] alone: its largest entries are next to -1, where bf16 is exact for
+// small probabilities; dh multiplies its fp32 sums by dloss, dw takes h already
 // multiplied by it (one rounding; one dloss for all rows multiplies the fp32 sums
-// instead).  With fewer entries the probabilities are near 2^-9 and above, dz's
-// largest entries are rounded anyway, and dloss goes into that same rounding.
-// Error against 64 bits over that of one rounding to bf16: dh 1.0, dw 1.3 to 1.4
-// from there on, both about 1.4 below (at 600 entries the wide way gives dw 1.7).
-// ---------------------------------------------------------------------------
+// instead).  With fewer entries the probabilities are near 2^-9 and above and one
+// rounding of dz would be as large as the outputs' own: dz (with dloss) is then
+// the sum of two bf16 numbers, a rounded value and what it left, and both products
+// run over both.  Error against 64 bits over that of one rounding to bf16: dh 1.0
+// everywhere, dw 1.0 below kCeWideV and up to 1.45 above (with one bf16 number it
+// was 1.3 to 1.6 for both below: 33 x 41 x 120, 35 x 365 x 1536).  The second
+// number costs 63 x 256 x 64 10.4 -> 13.1 us, 4096 x 1000 x 2560 54 -> 87 us.
 constexpr int64_t kCeWideV = 2048;
 constexpr int kCeMaxPairs = 96;
 constexpr int kCeMaxTiles = 4096;
 constexpr int kCeTileCost = 4;  // of a tile beside its blocks, in blocks: filling the pipe, the last epilogue
 
 struct CeBwdParams {
-  CUtensorMap dz_out, dw_out, dh_out, acc_out;  // of the stores: bf16 boxes of 64 x 32 rows, acc: fp32, 32 x 32
+  CUtensorMap dz_out, dw_out, dh_out;  // of the stores: bf16 boxes of 64 x 32 rows
+  CUtensorMap acc_out, dw_sum_out;     // fp32, 32 x 32
   int t, d;
   int zv, vv;           // entries of the next piece (dz) and of this one (dh, dw); 0: none
   int64_t zfirst, vfirst;
@@ -212,8 +215,10 @@ struct CeBwdParams {
   const float* lse;
   const float* dloss;
   int64_t dloss_stride;
-  int dz_scaled;        // dz holds dloss
-  int slices, k_run;
+  int planes;           // 2: dz holds dloss and is the sum of two numbers, `lo` columns apart; else 1
+  int lo;
+  int slices, k_run;        // dh's sum over the vocabulary: blocks of 64 a slice
+  int dw_slices, dw_run;    // dw's over the tokens; more than one: fp32 sums of [slices][v up to a multiple of 32][d]
   const float* acc;     // [slices][t up to a multiple of 32][d] fp32 sums of dh, or nullptr: dh is written directly
   int add;              // acc holds the earlier pieces' sum
   int last;             // with one slice: write dh instead of acc
@@ -242,12 +247,15 @@ struct CfgCeBwd {
   static constexpr int OUT_BYTES = EPI_WARPS * 2 * 4096;  // two boxes of 32 rows x 128 bytes a warp
   static constexpr int ACC_COLS = BN;
   static constexpr int TMEM_COLS = 512;
-  enum { kDz = 0, kDw = 1, kDh = 2 };  // a tile's problem; kDh + slice for dh
+  enum { kDz = 0, kDw = 1, kDh = 2 };  // a tile's problem: kind + 4 * slice
 
   __host__ __device__ static int up(int a, int b) { return (a + b - 1) / b; }
   __host__ __device__ static int tiles_dz(const Params& p) { return up(p.t, 256) * up(p.zv, 256); }
   __host__ __device__ static int tiles_dh(const Params& p) { return p.vv ? up(p.t, 256) * up(p.d, 256) * p.slices : 0; }
-  __host__ __device__ static int tiles_dw(const Params& p) { return up(p.vv, 256) * up(p.d, 256); }
+  __host__ __device__ static int tiles_dw(const Params& p) { return up(p.vv, 256) * up(p.d, 256) * p.dw_slices; }
+  // a product's blocks of 64: those of the rounded dz, then those of what it left
+  __host__ __device__ static int depth_dh(const Params& p) { return up(p.vv, BK) * p.planes; }
+  __host__ __device__ static int depth_dw(const Params& p) { return up(p.t, BK) * p.planes; }
 
   struct Tiles {
     __device__ static int count(const Params& p, int pair, int npairs) {
@@ -262,10 +270,14 @@ struct CfgCeBwd {
       if (id < tiles_dh(p)) {
         const int slice = id / (mt * nd);
         id -= slice * mt * nd;
-        return PairTile{kDh + slice, id % mt, id / mt, min(up(p.vv, BK) - slice * p.k_run, p.k_run)};
+        return PairTile{kDh + 4 * slice, id % mt, id / mt, min(depth_dh(p) - slice * p.k_run, p.k_run)};
       }
       id -= tiles_dh(p);
-      if (id < tiles_dw(p)) return PairTile{kDw, id % mv, id / mv, up(p.t, BK)};
+      if (id < tiles_dw(p)) {
+        const int slice = id / (mv * nd);
+        id -= slice * mv * nd;
+        return PairTile{kDw + 4 * slice, id % mv, id / mv, min(depth_dw(p) - slice * p.dw_run, p.dw_run)};
+      }
       id -= tiles_dw(p);
       return PairTile{kDz, id % mt, id / mt, up(p.d, BK)};
     }
@@ -275,23 +287,25 @@ struct CfgCeBwd {
   __device__ static void load_stage(const CUtensorMap* th, const CUtensorMap* tw, const CUtensorMap* tz,
                                     const CUtensorMap* ths, const Params& p, int prob, uint8_t* sA, uint8_t* sB,
                                     uint8_t*, int m0, int n0, int kb, uint64_t* bar) {
-    int k0 = kb * BK;
     if (prob == kDz) {
-      const int w0 = int(p.zfirst) + n0;
+      const int k0 = kb * BK, w0 = int(p.zfirst) + n0;
       tma_load_2d_pair(sA, th, k0, m0, bar);  // [64 m][64 k] x 2
       tma_load_2d_pair(sA + 8192, th, k0, m0 + 64, bar);
       tma_load_2d_pair(sB, tw, k0, w0, bar);
       tma_load_2d_pair(sB + 8192, tw, k0, w0 + 64, bar);
-    } else if (prob == kDw) {
-      tma_load_2d_pair(sA, tz, m0, k0, bar);  // [64 k][64 m] x 2
-      tma_load_2d_pair(sA + 8192, tz, m0 + 64, k0, bar);
+    } else if ((prob & 3) == kDw) {
+      kb += (prob >> 2) * p.dw_run;
+      const int half = up(p.t, BK), k0 = (kb < half ? kb : kb - half) * BK, x = m0 + (kb < half ? 0 : p.lo);
+      tma_load_2d_pair(sA, tz, x, k0, bar);  // [64 k][64 m] x 2
+      tma_load_2d_pair(sA + 8192, tz, x + 64, k0, bar);
       tma_load_2d_pair(sB, ths, n0, k0, bar);
       tma_load_2d_pair(sB + 8192, ths, n0 + 64, k0, bar);
     } else {
-      k0 += (prob - kDh) * p.k_run * BK;
+      kb += (prob >> 2) * p.k_run;
+      const int half = up(p.vv, BK), k0 = (kb < half ? kb : kb - half) * BK, x = k0 + (kb < half ? 0 : p.lo);
       const int w0 = int(p.vfirst) + k0;
-      tma_load_2d_pair(sA, tz, k0, m0, bar);  // [64 m][64 k] x 2
-      tma_load_2d_pair(sA + 8192, tz, k0, m0 + 64, bar);
+      tma_load_2d_pair(sA, tz, x, m0, bar);  // [64 m][64 k] x 2
+      tma_load_2d_pair(sA + 8192, tz, x, m0 + 64, bar);
       tma_load_2d_pair(sB, tw, n0, w0, bar);  // [64 k][64 n] x 2
       tma_load_2d_pair(sB + 8192, tw, n0 + 64, w0, bar);
     }
@@ -301,7 +315,7 @@ struct CfgCeBwd {
   // below the 512 cycles its MMAs take: the loop over a tile's stages is
   // compiled once for each kind, with constant descriptors.
   static constexpr int MMA_KINDS = 3;
-  __device__ static int mma_kind(int prob) { return min(prob, int(kDh)); }
+  __device__ static int mma_kind(int prob) { return prob & 3; }
   template <int KIND>
   __device__ static void mma_stage(uint32_t d_tmem, uint8_t* sA, uint8_t* sB, bool first) {
     constexpr bool a_mn = KIND == kDw, b_mn = KIND != kDz;
@@ -377,43 +391,46 @@ struct CfgCeBwd {
   __device__ static void epilogue(const Params& p, int prob, uint32_t t_acc, int row0, int n0, int lane, uint8_t* box,
                                   int part, int parts) {
     int turn = 0;
-    const bool dz = prob == kDz, dw = prob == kDw;
-    const int rows = dw ? p.vv : p.t, cols = dz ? p.zv : p.d;
+    const bool dz = prob == kDz, dw = (prob & 3) == kDw;
+    const int rows = dw ? p.vv : p.t;
     if (row0 >= rows) return;
     if (lane == 0) bulk_store_wait_read<0>();  // the tile before
     const int row = row0 + lane;
     const bool in = row < rows;
-    if (!dz && !dw && p.acc != nullptr && !p.last) {  // dh's fp32 sums: stored by the first piece, then added to
-      const int y = (prob - kDh) * up(p.t, 32) * 32 + row0;
+    // fp32 sums.  dh's: stored by the first piece, then added to
+    if (dw ? p.dw_slices > 1 : !dz && p.acc != nullptr && !p.last) {
+      const int y = (prob >> 2) * up(rows, 32) * 32 + row0;
 #pragma unroll 1
       for (int c = part; c < BN / 32; c += parts, turn ^= 4096) {
         uint32_t r[32];
         __syncwarp();
         tmem_load_32x32b_x32(t_acc + c * 32, r);
         tmem_load_wait();
-        if (n0 + c * 32 >= cols) break;
-        put(&p.acc_out, r, box + turn, lane, n0 + c * 32, y, p.add);
+        if (n0 + c * 32 >= p.d) break;
+        put(dw ? &p.dw_sum_out : &p.acc_out, r, box + turn, lane, n0 + c * 32, y, !dw && p.add);
       }
       return;
     }
     const int64_t target = !dw && in ? __ldcg(p.targets + row) : p.ignore;
     const bool live = good(p, target);
-    float factor = 0.0f, lse = 0.0f;
     if (dz) {
       if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0 && part == 0)
         raise_status(p.status, SBL_STATUS_BAD_TARGET);
-      if (live) lse = __ldcg(p.lse + row);
-      factor = live && p.dz_scaled ? __ldcg(p.dloss + row) : 1.0f;
-    } else if (dw) {
-      factor = p.dloss_stride == 0 ? __ldcg(p.dloss) : 1.0f;
-    } else if (live) {
-      factor = p.dz_scaled ? 1.0f : __ldcg(p.dloss + row * p.dloss_stride);
+      if (p.planes > 1)
+        dz_tile<2>(p, t_acc, row0, n0, lane, box, part, parts, target, live);
+      else
+        dz_tile<1>(p, t_acc, row0, n0, lane, box, part, parts, target, live);
+      return;
     }
-    const CUtensorMap* map = dz ? &p.dz_out : dw ? &p.dw_out : &p.dh_out;
+    float factor = 0.0f;
+    if (dw)
+      factor = p.planes == 1 && p.dloss_stride == 0 ? __ldcg(p.dloss) : 1.0f;
+    else if (live)
+      factor = p.planes > 1 ? 1.0f : __ldcg(p.dloss + row * p.dloss_stride);
 #pragma unroll 1
     for (int c = part; c < BN / 64; c += parts, turn ^= 4096) {
       const int col0 = n0 + c * 64;
-      if (col0 >= cols) break;  // uniform across the warp
+      if (col0 >= p.d) break;  // uniform across the warp
       uint32_t word[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -421,97 +438,169 @@ struct CfgCeBwd {
         __syncwarp();
         tmem_load_32x32b_x32(t_acc + c * 64 + h * 32, r);
         tmem_load_wait();
-        if (dz) {
-          const int64_t at = target - p.zfirst - col0 - h * 32;
+        if (!dw && p.add && in) {  // dh's last piece.  Through L2: another SM wrote it in the launch before
+          const float* acc = p.acc + int64_t(row) * p.d + col0 + h * 32;
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float x = exp_of(__uint_as_float(r[e]) - lse);
-            if (at == e) x -= 1.0f;
-            r[e] = __float_as_uint(live ? x * factor : 0.0f);
-          }
-        } else {
-          if (!dw && p.add && in) {  // dh's last piece.  Through L2: another SM wrote it in the launch before
-            const float* acc = p.acc + int64_t(row) * p.d + col0 + h * 32;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (col0 + h * 32 + 4 * q >= p.d) break;
-              const float4 a = __ldcg(reinterpret_cast<const float4*>(acc) + q);
-              r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + a.x);
-              r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + a.y);
-              r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + a.z);
-              r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + a.w);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * factor);
-          if (!dw && !live) {  // whatever the sums of a row without loss are (zero, but for NaN operands)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          for (int q = 0; q < 8; ++q) {
+            if (col0 + h * 32 + 4 * q >= p.d) break;
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(acc) + q);
+            r[4 * q] = __float_as_uint(__uint_as_float(r[4 * q]) + a.x);
+            r[4 * q + 1] = __float_as_uint(__uint_as_float(r[4 * q + 1]) + a.y);
+            r[4 * q + 2] = __float_as_uint(__uint_as_float(r[4 * q + 2]) + a.z);
+            r[4 * q + 3] = __float_as_uint(__uint_as_float(r[4 * q + 3]) + a.w);
           }
         }
+        const bool none = !dw && !live;  // a row without loss: zero whatever its sums are (NaN weights)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
-          word[16 * h + e] = *reinterpret_cast<const uint32_t*>(&h2);
+          const uint32_t u = pack_bf16(__uint_as_float(r[2 * e]) * factor, __uint_as_float(r[2 * e + 1]) * factor);
+          word[16 * h + e] = none ? 0u : u;
         }
       }
-      put(map, word, box + turn, lane, col0, row0, false);
+      put(dw ? &p.dw_out : &p.dh_out, word, box + turn, lane, col0, row0, false);
+    }
+  }
+
+  __device__ static __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h2);
+  }
+
+  // dz's tile.  One plane: two boxes in turn, as above.  Two: one box holds the
+  // rounded values, the other what they left.
+  template <int PLANES>
+  __device__ static __forceinline__ void dz_tile(const Params& p, uint32_t t_acc, int row0, int n0, int lane,
+                                                 uint8_t* box, int part, int parts, int64_t target, bool live) {
+    const int row = row0 + lane;
+    const float lse = live ? __ldcg(p.lse + row) : 0.0f;
+    const float factor = PLANES > 1 && live ? __ldcg(p.dloss + row * p.dloss_stride) : 1.0f;
+#pragma unroll 1
+    for (int c = part; c < BN / 64; c += parts) {
+      const int col0 = n0 + c * 64;
+      if (col0 >= p.zv) break;  // uniform across the warp
+      if (lane == 0) bulk_store_wait_read<PLANES == 1 ? 1 : 0>();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_load_32x32b_x32(t_acc + c * 64 + h * 32, r);
+        tmem_load_wait();
+        const int64_t at = target - p.zfirst - col0 - h * 32;
+        const int left = p.zv - col0 - h * 32;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float x = exp_of(__uint_as_float(r[e]) - lse);
+          if (at == e) x -= 1.0f;
+          // columns past the piece: beside a second plane they are read as part of its last block
+          const bool none = PLANES > 1 ? !live || e >= left : !live;
+          r[e] = none ? 0u : __float_as_uint(x * factor);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t u[4], v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(r[8 * q + 2 * e]), y = __uint_as_float(r[8 * q + 2 * e + 1]);
+            u[e] = pack_bf16(x, y);
+            if constexpr (PLANES > 1)
+              v[e] = pack_bf16(x - __uint_as_float(u[e] << 16), y - __uint_as_float(u[e] & 0xFFFF0000u));
+          }
+          uint8_t* dst = box + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+          if constexpr (PLANES > 1) *reinterpret_cast<uint4*>(dst + 4096) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&p.dz_out, box, col0, row0);
+        if constexpr (PLANES > 1) tma_store_2d(&p.dz_out, box + 4096, col0 + p.lo, row0);
+        bulk_store_commit();
+      }
+      if constexpr (PLANES == 1) box = (c - part) / parts & 1 ? box - 4096 : box + 4096;
     }
   }
 };
 
-// dh = dloss (1 where dz holds it) times the sum of its slices, in their order: 4 elements a thread.
+// The slices of dh and of dw added in their order, 4 elements a thread.  dh's rows
+// are multiplied by their dloss (dloss NULL: dz held it), dw by the one dloss there
+// is for all rows (dw_factor; NULL: 1).
+struct CeSum {
+  const float4* part;  // [slices][slice_n4]
+  int slices;
+  int64_t slice_n4, n4;  // n4 0: not split, nothing to do
+  uint2* out;
+};
+
 __global__ void __launch_bounds__(256)
-    k_ce_dh(const float4* __restrict__ acc, int slices, int64_t slice_n4, int64_t n4, int row_n4,
-            const int64_t* __restrict__ targets, const float* __restrict__ dloss, int64_t dloss_stride, int64_t v,
-            int64_t ignore, uint2* __restrict__ dh) {
+    k_ce_sum(const CeSum dh, const CeSum dw, unsigned dh_blocks, int row_n4, const int64_t* __restrict__ targets,
+             const float* __restrict__ dloss, int64_t dloss_stride, const float* __restrict__ dw_factor, int64_t v,
+             int64_t ignore) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const int64_t row = i / row_n4, target = targets[row];
-  const bool live = target >= 0 && target < v && target != ignore;
-  const float g = !live ? 0.0f : dloss != nullptr ? dloss[row * dloss_stride] : 1.0f;
-  float4 a = __ldcg(acc + i);
-  for (int s = 1; s < slices; ++s) {
-    const float4 b = __ldcg(acc + s * slice_n4 + i);
+  const bool first = blockIdx.x < dh_blocks;
+  const CeSum& s = first ? dh : dw;
+  const int64_t i = int64_t(blockIdx.x - (first ? 0u : dh_blocks)) * 256 + threadIdx.x;
+  if (i >= s.n4) return;
+  float g = 1.0f;
+  bool live = true;
+  if (first) {
+    const int64_t row = i / row_n4, target = targets[row];
+    live = target >= 0 && target < v && target != ignore;
+    if (live && dloss != nullptr) g = dloss[row * dloss_stride];
+  } else if (dw_factor != nullptr) {
+    g = *dw_factor;
+  }
+  float4 a = __ldcg(s.part + i);
+  for (int k = 1; k < s.slices; ++k) {
+    const float4 b = __ldcg(s.part + k * s.slice_n4 + i);
     a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
   }
   const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * g, a.y * g), hi = __floats2bfloat162_rn(a.z * g, a.w * g);
-  dh[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  s.out[i] = live ? make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi))
+                  : make_uint2(0u, 0u);
 }
 
 // How the backward pass cuts its work.
 constexpr int64_t kCeDzBytes = int64_t(64) << 20;  // dz of one piece: half of L2
 
 struct CePlan {
+  int planes;       // numbers that a dz is the sum of
   int64_t piece;    // vocabulary entries of a piece, a multiple of 256
   int64_t pieces;
-  int slices, k_run;
-  int64_t acc_rows;  // rows of a slice of dh's sums: t up to a multiple of the 32 that a store writes
-  uint64_t dz_bytes, acc_bytes, scaled_bytes;  // dz: one buffer of two (one piece: of one)
-  uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + scaled_bytes; }
+  int slices, k_run, dw_slices, dw_run;
+  int64_t acc_rows, dw_rows;  // rows of a slice of the sums: t and v up to a multiple of the 32 that a store writes
+  uint64_t dz_bytes, acc_bytes, dw_bytes, scaled_bytes;  // dz: one buffer of two (one piece: of one)
+  uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + dw_bytes + scaled_bytes; }
 };
 
 CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   CePlan c;
   const int64_t padded = (v + 255) / 256 * 256;
-  const int64_t most = std::max<int64_t>(kCeDzBytes / (2 * t) / 256, 1) * 256;
+  c.planes = v < kCeWideV ? 2 : 1;
+  const int64_t most = std::max<int64_t>(kCeDzBytes / (2 * c.planes * t) / 256, 1) * 256;
   c.pieces = (padded + most - 1) / most;
   c.piece = ((padded / 256 + c.pieces - 1) / c.pieces) * 256;  // even pieces
   c.pieces = (padded + c.piece - 1) / c.piece;
-  c.dz_bytes = align_up(uint64_t(t) * uint64_t(c.piece) * 2, 256);
+  c.dz_bytes = align_up(uint64_t(t) * uint64_t(c.piece) * 2 * c.planes, 256);
   c.scaled_bytes = align_up(uint64_t(t) * uint64_t(d) * 2, 256);
-  // A dh tile is as deep as the piece is wide.  A run of the sum is at most
-  // what each pair of SMs has to do anyway (or 8 blocks).
+  // A dh tile is as deep as the piece is wide, a dw tile as there are tokens.  A
+  // run of the sum is about what each pair of SMs has to do anyway (or 8 blocks).
+  // dw is split where it has few tiles (one piece) and would take twice as long
+  // (4096 x 256 x 2560: 69 -> 48 us, 16384 x 256 x 1024: 205 -> 71).
   const int64_t nb = (d + 255) / 256, mb0 = (t + 255) / 256, mb1 = c.piece / 256;
-  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64, kb1 = (t + 63) / 64, pairs = 74;  // 148 SMs
+  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64 * c.planes, kb1 = (t + 63) / 64 * c.planes, pairs = 74;  // 148 SMs
   const int64_t share = std::max<int64_t>((mb0 * nb * kb0 + mb1 * nb * kb1) / pairs, 8);
   int64_t slices = std::min<int64_t>((kb0 + share - 1) / share, 32);
   c.k_run = static_cast<int>((kb0 + slices - 1) / slices);
   c.slices = static_cast<int>((kb0 + c.k_run - 1) / c.k_run);
   c.acc_rows = (t + 31) / 32 * 32;
   const uint64_t acc = uint64_t(c.slices) * uint64_t(c.acc_rows) * uint64_t(d) * 4;
+  const int64_t dw_slices = c.pieces > 1 ? 1 : std::min<int64_t>(std::max<int64_t>(kb1 / share, 1), 32);
+  c.dw_run = static_cast<int>((kb1 + dw_slices - 1) / dw_slices);
+  c.dw_slices = static_cast<int>((kb1 + c.dw_run - 1) / c.dw_run);
+  c.dw_rows = (v + 31) / 32 * 32;
+  c.dw_bytes = c.dw_slices > 1 ? align_up(uint64_t(c.dw_slices) * uint64_t(c.dw_rows) * uint64_t(d) * 4, 256) : 0;
   c.acc_bytes = c.pieces > 1 || c.slices > 1 ? align_up(acc, 256) : 0;
   return c;
 }
@@ -615,14 +704,18 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
   ws += c.dz_bytes * (c.pieces > 1 ? 2 : 1);
   float* acc = c.acc_bytes ? reinterpret_cast<float*>(ws) : nullptr;
   ws += c.acc_bytes;
-  const bool dz_scaled = a.dloss_stride != 0 && a.v < kCeWideV;
+  float* dw_sum = c.dw_bytes ? reinterpret_cast<float*>(ws) : nullptr;
+  ws += c.dw_bytes;
   uint16_t* scaled = reinterpret_cast<uint16_t*>(ws);  // dw's operand
   cudaError_t e;
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd<4>>(num_sms, &max_clusters)) != cudaSuccess) return e;
-  CUtensorMap th, tw, ths, dh_out, acc_out;
+  CUtensorMap th, tw, ths, dh_out, acc_out, dw_sum_out;
   if (acc != nullptr && !encode_tmap_2d(&acc_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, acc, a.d, c.slices * c.acc_rows,
                                         a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (dw_sum != nullptr && !encode_tmap_2d(&dw_sum_out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dw_sum, a.d,
+                                           c.dw_slices * c.dw_rows, a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!rows_map(&dh_out, dh, a.d, a.t, a.d, 32) || !rows_map(&th, h, a.d, a.t, a.d, 64) ||
       !rows_map(&tw, w, a.d, a.v, a.d, 64) ||
@@ -630,28 +723,33 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
   for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
+    using Cfg = CfgCeBwd<4>;
     CeBwdParams p;
     p.t = static_cast<int>(a.t), p.d = static_cast<int>(a.d);
     p.zv = static_cast<int>(wide(i + 1)), p.zfirst = (i + 1) * c.piece;
     p.vv = static_cast<int>(wide(i)), p.vfirst = i * c.piece;
     p.targets = a.targets, p.v_all = a.v, p.ignore = a.ignore_index;
-    p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride, p.dz_scaled = dz_scaled;
-    p.k_run = c.k_run;
-    p.slices = ((p.vv + 63) / 64 + c.k_run - 1) / c.k_run;
+    p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride;
+    p.planes = c.planes, p.lo = static_cast<int>(c.piece);
+    p.k_run = c.k_run, p.dw_slices = c.dw_slices, p.dw_run = c.dw_run;
+    p.slices = (Cfg::depth_dh(p) + c.k_run - 1) / c.k_run;
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
     p.h = h, p.scaled = i < 0 ? scaled : nullptr;
-    p.row_factor = a.dloss_stride != 0 && !dz_scaled;  // else dz holds dloss, or it multiplies the sums
+    p.row_factor = a.dloss_stride != 0 && c.planes == 1;  // else dz holds dloss, or it multiplies the sums
     p.status = a.status_dev;
     CUtensorMap tz = th;
-    p.dz_out = p.dw_out = p.acc_out = p.dh_out = dh_out;
-    if (p.zv > 0 && !rows_map(&p.dz_out, dz[(i + 1) & 1], p.zv, a.t, c.piece, 32)) return cudaErrorInvalidValue;
-    if (p.vv > 0 && (!rows_map(&tz, dz[i & 1], p.vv, a.t, c.piece, 64) ||
+    p.dz_out = p.dw_out = p.acc_out = p.dw_sum_out = p.dh_out = dh_out;
+    const auto dz_map = [&](CUtensorMap* map, int64_t j, int64_t cols, int box_rows) {
+      return rows_map(map, dz[j & 1], c.planes > 1 ? 2 * c.piece : cols, a.t, c.planes * c.piece, box_rows);
+    };
+    if (p.zv > 0 && !dz_map(&p.dz_out, i + 1, p.zv, 32)) return cudaErrorInvalidValue;
+    if (p.vv > 0 && (!dz_map(&tz, i, p.vv, 64) ||
                      !rows_map(&p.dw_out, dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
       return cudaErrorInvalidValue;
     if (acc != nullptr) p.acc_out = acc_out;
-    using Cfg = CfgCeBwd<4>;
+    if (dw_sum != nullptr) p.dw_sum_out = dw_sum_out;
     const int n_dh = Cfg::tiles_dh(p), n_dw = Cfg::tiles_dw(p), n_dz = Cfg::tiles_dz(p);
     const int64_t tiles = int64_t(n_dh) + n_dw + n_dz;
     // the first launch has a warp for each row to copy too, if need be on pairs without a tile
@@ -659,17 +757,22 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     const int pairs = static_cast<int>(std::min<int64_t>({busy, max_clusters, kCeMaxPairs}));
     p.tabled = tiles <= kCeMaxTiles;
     if (p.tabled)
-      ce_schedule(n_dh, std::min(c.k_run, (p.vv + 63) / 64), n_dw, (p.t + 63) / 64, n_dz, (p.d + 63) / 64, pairs, p);
+      ce_schedule(n_dh, std::min(c.k_run, Cfg::depth_dh(p)), n_dw, std::min(c.dw_run, Cfg::depth_dw(p)), n_dz, (p.d + 63) / 64, pairs, p);
     e = tiles <= pairs ? launch_ce_tiles<8>(th, tw, tz, ths, p, pairs, num_sms, s)
                        : launch_ce_tiles<4>(th, tw, tz, ths, p, pairs, num_sms, s);
     if (e != cudaSuccess) return e;
   }
-  if (c.slices > 1) {
-    const int64_t n4 = a.t * a.d / 4;
-    return launch_pdl(k_ce_dh, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, s,
-                      reinterpret_cast<const float4*>(acc), c.slices, c.acc_rows * a.d / 4, n4,
-                      static_cast<int>(a.d / 4), a.targets, dz_scaled ? nullptr : a.dloss, a.dloss_stride, a.v,
-                      a.ignore_index, reinterpret_cast<uint2*>(dh));
+  if (c.slices > 1 || c.dw_slices > 1) {
+    CeSum h_sum{reinterpret_cast<const float4*>(acc), c.slices, c.acc_rows * a.d / 4, 0, reinterpret_cast<uint2*>(dh)};
+    CeSum w_sum{reinterpret_cast<const float4*>(dw_sum), c.dw_slices, c.dw_rows * a.d / 4, 0,
+                reinterpret_cast<uint2*>(dw)};
+    if (c.slices > 1) h_sum.n4 = a.t * a.d / 4;
+    if (c.dw_slices > 1) w_sum.n4 = a.v * a.d / 4;
+    const unsigned h_blocks = static_cast<unsigned>((h_sum.n4 + 255) / 256),
+                   w_blocks = static_cast<unsigned>((w_sum.n4 + 255) / 256);
+    return launch_pdl(k_ce_sum, dim3(h_blocks + w_blocks), dim3(256), 0, s, h_sum, w_sum, h_blocks,
+                      static_cast<int>(a.d / 4), a.targets, c.planes > 1 ? nullptr : a.dloss, a.dloss_stride,
+                      c.planes == 1 && a.dloss_stride == 0 ? a.dloss : nullptr, a.v, a.ignore_index);
   }
   return cudaSuccess;
 }

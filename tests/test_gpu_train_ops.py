@@ -677,6 +677,41 @@ def test_linear_ce_backward_in_pieces(t, v, d):
     check_ce_bwd(dh, dw, h, w, y, lse, dloss)
 
 
+@pytest.mark.parametrize("one", [False, True], ids=["each", "one"])
+@pytest.mark.parametrize("t,v,d", [(3000, 40, 64), (5001, 300, 72), (9000, 2100, 64), (16384, 256, 136), (2100, 17, 2560)])
+def test_linear_ce_backward_of_many_tokens(t, v, d, one):
+    """dw has few tiles and a long sum over the tokens, which is split and joined."""
+    h, w, y = ce_inputs(t, v, d, 12)
+    loss, lse = ce_forward(h, w, y)
+    dloss = randn(1 if one else t, seed=9, std=0.3, mean=1.0)
+    launched = sbl.launch_count()
+    dh, dw = ce_backward(h, w, y, lse, dloss)
+    assert sbl.launch_count() - launched == 3
+    check_ce_bwd(dh, dw, h, w, y, lse, dloss)
+    again = ce_backward(h, w, y, lse, dloss)
+    assert same_bits(again[0], dh) and same_bits(again[1], dw)
+
+
+@pytest.mark.parametrize("t,v,d", [(33, 41, 120), (300, 365, 264), (1, 180, 1120), (2000, 2047, 64)])
+def test_linear_ce_backward_of_few_entries_is_as_exact_as_its_outputs(t, v, d):
+    """Below 2048 entries the products' operands are exact to 2^-17: what is left is the outputs' one rounding."""
+    h, w, y = ce_inputs(t, v, d, 13)
+    loss, lse = ce_forward(h, w, y)
+    dloss = randn(t, seed=9, std=0.3, mean=1.0)
+    dh, dw = ce_backward(h, w, y, lse, dloss)
+    p = (h.double() @ w.double().T - lse.double()[:, None]).exp()
+    live = y != -100
+    p[live] -= torch.nn.functional.one_hot(y[live], v).double()
+    dz = p * torch.where(live, dloss.double(), 0.0)[:, None]
+    off = 2.0 ** -17 * dz.abs() + p.abs().clamp_max(1.0) * dloss.double().abs()[:, None] * (
+        logit_bound(h, w) + 8 * U * lse.double().abs()[:, None] + 2.0 ** -20)
+    for got, a, b, n in ((dh, dz, w.double(), v), (dw, dz.T, h.double(), t)):
+        want, terms = a @ b, a.abs() @ b.abs()
+        tol = (off if got is dh else off.T) @ b.abs() + (n / 8 + 65) * 2 * U * terms
+        # the bound of every element: its own rounding, the operands' 2^-17, the logits' errors, the sums
+        assert ((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all()
+
+
 def test_linear_ce_backward_of_many_tiles():
     """More output tiles than the launch's table of tiles holds: they are striped over the SMs instead."""
     t, v, d = 256, 40000, 8192
