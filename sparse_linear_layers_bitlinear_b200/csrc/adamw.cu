@@ -16,9 +16,9 @@
 // the next step divide by eps.
 //
 // Measured, the 79 M weights of a transformer block (four 2560 x 2560, three 6912 x
-// 2560, vectors) in one launch: fp32 states 332 us (6.7 TB/s, the copy's rate);
-// 8-bit states 222 us (5.7 TB/s; 53 instructions a weight, two reductions a block
-// among them, keep the schedulers 58 % busy).
+// 2560, vectors) in one launch: fp32 states 327 us (6.8 TB/s, a little over
+// the copy's rate); 8-bit states 205 us (6.2 TB/s; 53 instructions a weight, two
+// reductions a block among them).
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -33,9 +33,12 @@ namespace sbl {
 
 namespace {
 
-constexpr int kAdamThreads = 256;
-// Elements of one tensor that a block updates: 16 a thread with fp32 states,
-// one 8-bit block a warp.
+// Blocks of 128 threads: with 8-bit states nine of them have 56 registers a thread
+// (79 M weights in a graph 190 us; four blocks of 256 with 64 registers 210, ten of
+// 128 with 48 and spills 203).  Elements of one tensor that a block updates: 16 a
+// thread with fp32 states (327 -> 324 us against blocks of 256, 95 k weights 5.9 ->
+// 3.7; 8 a thread 325 and 5.1), one 8-bit block a warp.
+constexpr int kAdamThreads = 128;
 constexpr int chunk_of(bool eight) { return eight ? kAdamThreads / 32 * SBL_ADAMW_BLOCK : 16 * kAdamThreads; }
 constexpr float kFlush = 0x1p-100f;
 constexpr float kFp8Max = 448.0f, kFp8Min = 0x1p-9f;
@@ -348,7 +351,7 @@ __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s
 }
 
 template <bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads, EIGHT ? 4 : 2) k_adamw(const __grid_constant__ AdamLaunch p) {
+__global__ void __launch_bounds__(kAdamThreads, EIGHT ? 9 : 4) k_adamw(const __grid_constant__ AdamLaunch p) {
   int lo = 0, hi = p.count - 1;  // the last tensor whose first chunk is not past this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

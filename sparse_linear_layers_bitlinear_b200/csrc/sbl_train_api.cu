@@ -136,7 +136,7 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
       for (int32_t i = 0; i < count; ++i) {
         const sbl_adamw_tensor& t = tensors[i];
         if (t.numel == 0 || (t.flags & SBL_ADAMW_STATE_8BIT) != kind) continue;
-        if ((n == kAdamMaxTensors || elements + uint64_t(t.numel) > (uint64_t(1) << 41)) && !launch())
+        if ((n == kAdamMaxTensors || elements + uint64_t(t.numel) > (uint64_t(1) << 40)) && !launch())
           return SBL_ERR_CUDA;
         batch[n++] = t;
         elements += uint64_t(t.numel);
