@@ -36,7 +36,7 @@ namespace {
 // Blocks of 128 threads: with 8-bit states nine of them have 56 registers a thread
 // (79 M weights in a graph 190 us; four blocks of 256 with 64 registers 210, ten of
 // 128 with 48 and spills 203).  Elements of one tensor that a block updates: 16 a
-// thread with fp32 states (327 -> 324 us against blocks of 256, 95 k weights 5.9 ->
+// thread with fp32 states (327 -> 324 us against blocks of 256, 90 k weights 5.9 ->
 // 3.7; 8 a thread 325 and 5.1), one 8-bit block a warp.
 constexpr int kAdamThreads = 128;
 constexpr int chunk_of(bool eight) { return eight ? kAdamThreads / 32 * SBL_ADAMW_BLOCK : 16 * kAdamThreads; }
