@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256)
 // rounding of dz would be as large as the outputs' own: dz (with dloss) is then
 // the sum of two bf16 numbers, a rounded value and what it left, and both products
 // run over both.  Error against 64 bits over that of one rounding to bf16: dh 1.0
-// everywhere, dw 1.0 below kCeWideV and up to 1.45 above (with one bf16 number it
+// everywhere, dw 1.0 below kCeWideV and up to 1.46 above (with one bf16 number it
 // was 1.3 to 1.6 for both below: 33 x 41 x 120, 35 x 365 x 1536); rows whose
 // probabilities are not small cost both one rounding of dz more there.  The second
 // number costs 63 x 256 x 64 10.4 -> 13.1 us, 4096 x 1000 x 2560 54 -> 87 us.
@@ -338,7 +338,7 @@ struct CfgCeBwd {
   // The first launch: dw's operand, h (or h times each row's dloss) with zeros in
   // the rows without loss, whose h may hold anything: zero times a NaN would reach
   // dw.  A row a warp, while the first tiles' products run (4096 x 2560: nothing
-  // beside 32768 entries, 2 us of 54 beside 1000; loads of several rows at once
+  // beside 32768 entries, 2 us beside 1000; loads of several rows at once
   // took no less).
   __device__ static void prologue(const Params& p, int warp, int warps, int lane) {
     if (p.scaled == nullptr) return;
