@@ -504,12 +504,10 @@ sbl_status sbl_linear_ce_forward(const sbl_linear_ce_args* args, sbl_stream_t st
  * loss, dloss[i * dloss_stride] (stride 0: one value for all rows).
  *   dz_ij = dloss_i (exp(z_ij - lse_i) - [j = target_i]), 0 for ignored rows and rows with a bad target
  *   dh = dz w,   dw = dz^T h
- * The logits are computed again, a piece of the vocabulary at a time.  For the
- * two products, which accumulate in fp32, dz becomes the sum of two bf16 numbers
- * below 2048 entries (2^-17 off at most); from there on exp(z - lse) - [j = target]
- * is rounded to bf16, and for dw also dloss_i h_i (with stride 0 dloss multiplies
- * the sums instead).  lse is fp32: a probability's relative error grows as
- * |lse| 2^-24.
+ * The logits are computed again, a piece of the vocabulary at a time.  The two
+ * products, which accumulate in fp32, take dz as the sum of two bf16 numbers, 2^-16
+ * off at most; the outputs are rounded once, to bf16.  lse is fp32: a probability's
+ * relative error grows as |lse| 2^-24.
  * `workspace`: sbl_linear_ce_workspace_bytes(t, v, d, 1) bytes, 256-byte
  * aligned.  Rows without loss give dh = 0 and add nothing to dw,
  * whatever their h, lse and dloss hold.

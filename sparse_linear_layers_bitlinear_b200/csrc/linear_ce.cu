@@ -11,16 +11,17 @@
 // sustained (the power cap holds the clock), 8192 x 32768 x 2560: 1020 us, 1350
 // TFLOP/s; the library's product alone, with its logits written: 1010 us.
 //
-// Backward, a piece of the vocabulary at a time, so that dz (bf16, at most
-// kCeDzBytes) stays in L2 between its writer and its two readers: a launch
+// Backward, a piece of the vocabulary at a time, so that dz (the sum of two bf16
+// numbers, see below) stays in L2 between its writer and its two readers: a launch
 // computes a piece's logits again and writes dz, and runs both products over
 // the piece before.  dw rows belong to one piece; dh adds up over the pieces
 // in fp32.  With few tokens dh has few output tiles and a long sum over the
 // vocabulary, with few entries dw a long one over the tokens; they are then split
 // over slices that a last launch joins.
-// Measured, sustained, 4096 x 32768 x 2560: 1.70 ms, 1210 TFLOP/s (three times
-// the library's product of this size in the same run: 1.52 ms); what is over are
-// dz's way through L2, dh's fp32 sums and the ends of the launches.
+// Measured, sustained, 4096 x 32768 x 2560: 2.88 ms, 1190 TFLOP/s over the five units
+// of 687 Gflop that dz's two numbers make of the three (the library's product of this
+// size in a run of its own: 0.51 ms); what is over are dz's way through L2, dh's fp32
+// sums and the ends of the launches.
 #include <algorithm>
 #include <array>
 #include <functional>
@@ -182,27 +183,21 @@ __global__ void __launch_bounds__(256)
 //        A = h [t][d], B = the piece's rows of w, both K-major, K = d
 //   dh   of this piece:  A = dz [t][v] K-major, B = w's rows MN-major, K = v,
 //        in `slices` runs of k_run blocks of 64
-//   dw   of this piece:  A = dz MN-major (M = v), B = the scaled h MN-major, K = t,
+//   dw   of this piece:  A = dz MN-major (M = v), B = h MN-major, K = t,
 //        in `dw_slices` runs of dw_run blocks
 // so that a piece costs one launch and the short tiles fill the gaps that the
 // deep ones leave.  Every operand is read in boxes of 64 x 64, which both
 // majors can use, so one tensor map each serves h, w and dz (boxes of 128 rows
 // for the K-major operands took the same time).
 //
-// How dz becomes bf16, and where a row's factor dloss goes, decides how many
-// roundings a product carries.  From kCeWideV entries on dz holds exp(z - lse) -
-// [j = target] alone: its largest entries are next to -1, where bf16 is exact for
-// small probabilities; dh multiplies its fp32 sums by dloss, dw takes h already
-// multiplied by it (one rounding; one dloss for all rows multiplies the fp32 sums
-// instead).  With fewer entries the probabilities are near 2^-9 and above and one
-// rounding of dz would be as large as the outputs' own: dz (with dloss) is then
-// the sum of two bf16 numbers, a rounded value and what it left, and both products
-// run over both.  Error against 64 bits over that of one rounding to bf16: dh 1.0
-// everywhere, dw 1.0 below kCeWideV and up to 1.46 above (with one bf16 number it
-// was 1.3 to 1.6 for both below: 33 x 41 x 120, 35 x 365 x 1536); rows whose
-// probabilities are not small cost both one rounding of dz more there.  The second
-// number costs 63 x 256 x 64 10.4 -> 13.1 us, 4096 x 1000 x 2560 54 -> 87 us.
-constexpr int64_t kCeWideV = 2048;
+// dz, dloss included, is held as the sum of two bf16 numbers: a rounded value and
+// what it left, so that it is exact to 2^-16, and both products run over both.  One
+// number would cost a rounding as large as the outputs' own wherever an output is
+// not ruled by an entry that bf16 holds exactly: over the error of the outputs'
+// rounding alone, dh then had 1.01 (flat rows) to 1.44 (median target probability
+// 0.63) and dw, whose operand h took dloss with a second rounding, 1.43 to 1.74.
+// With two numbers it is 1.00 for both.  The price is five units of product
+// instead of three.
 constexpr int kCeMaxPairs = 96;
 constexpr int kCeMaxTiles = 4096;
 constexpr int kCeTileCost = 4;  // of a tile beside its blocks, in blocks: filling the pipe, the last epilogue
@@ -218,16 +213,14 @@ struct CeBwdParams {
   const float* lse;
   const float* dloss;
   int64_t dloss_stride;
-  int planes;           // 2: dz holds dloss and is the sum of two numbers, `lo` columns apart; else 1
-  int lo;
+  int lo;               // columns from a dz's rounded value to what it left
   int slices, k_run;        // dh's sum over the vocabulary: blocks of 64 a slice
   int dw_slices, dw_run;    // dw's over the tokens; more than one: fp32 sums of [slices][v up to a multiple of 32][d]
   const float* acc;     // [slices][t up to a multiple of 32][d] fp32 sums of dh, or nullptr: dh is written directly
   int add;              // acc holds the earlier pieces' sum
   int last;             // with one slice: write dh instead of acc
   const uint16_t* h;
-  uint16_t* scaled;     // the first launch: where dw's operand goes (else nullptr)
-  int row_factor;       // dw's operand is h times dloss, else h
+  uint16_t* live_h;     // the first launch: where dw's operand goes (else nullptr)
   uint32_t* status;
   int tabled;           // tiles from the table, else striped
   uint16_t sched_off[kCeMaxPairs + 1];
@@ -257,8 +250,8 @@ struct CfgCeBwd {
   __host__ __device__ static int tiles_dh(const Params& p) { return p.vv ? up(p.t, 256) * up(p.d, 256) * p.slices : 0; }
   __host__ __device__ static int tiles_dw(const Params& p) { return up(p.vv, 256) * up(p.d, 256) * p.dw_slices; }
   // a product's blocks of 64: those of the rounded dz, then those of what it left
-  __host__ __device__ static int depth_dh(const Params& p) { return up(p.vv, BK) * p.planes; }
-  __host__ __device__ static int depth_dw(const Params& p) { return up(p.t, BK) * p.planes; }
+  __host__ __device__ static int depth_dh(const Params& p) { return 2 * up(p.vv, BK); }
+  __host__ __device__ static int depth_dw(const Params& p) { return 2 * up(p.t, BK); }
 
   struct Tiles {
     __device__ static int count(const Params& p, int pair, int npairs) {
@@ -335,33 +328,20 @@ struct CfgCeBwd {
     return target >= 0 && target < p.v_all && target != p.ignore;
   }
 
-  // The first launch: dw's operand, h (or h times each row's dloss) with zeros in
-  // the rows without loss, whose h may hold anything: zero times a NaN would reach
-  // dw.  A row a warp, while the first tiles' products run (4096 x 2560: nothing
-  // beside 32768 entries, 2 us beside 1000; loads of several rows at once
-  // took no less).
+  // The first launch: dw's operand, h with zeros in the rows without loss, whose h
+  // may hold anything: zero times a NaN would reach dw.  A row a warp, while the
+  // first tiles' products run (4096 x 2560: nothing beside 32768 entries, 2 us
+  // beside 1000; loads of several rows at once took no less).
   __device__ static void prologue(const Params& p, int warp, int warps, int lane) {
-    if (p.scaled == nullptr) return;
-    pdl_wait();  // h, targets and dloss may come from the kernel before
+    if (p.live_h == nullptr) return;
+    pdl_wait();  // h and targets may come from the kernel before
     const int vecs = p.d / 8;
     for (int row = warp; row < p.t; row += warps) {
       const bool live = good(p, __ldcg(p.targets + row));
-      const float g = live && p.row_factor ? __ldcg(p.dloss + row) : 1.0f;
       const uint4* src = reinterpret_cast<const uint4*>(p.h) + int64_t(row) * vecs;
-      uint4* dst = reinterpret_cast<uint4*>(p.scaled) + int64_t(row) * vecs;
+      uint4* dst = reinterpret_cast<uint4*>(p.live_h) + int64_t(row) * vecs;
 #pragma unroll 4
-      for (int i = lane; i < vecs; i += 32) {
-        const uint4 x = __ldcg(src + i);
-        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 h2 =
-              __floats2bfloat162_rn(__uint_as_float(in[e] << 16) * g, __uint_as_float(in[e] & 0xFFFF0000u) * g);
-          o[e] = live ? *reinterpret_cast<const uint32_t*>(&h2) : 0u;
-        }
-        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+      for (int i = lane; i < vecs; i += 32) dst[i] = live ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
 
@@ -419,17 +399,9 @@ struct CfgCeBwd {
     if (dz) {
       if (in && !live && target != p.ignore && n0 == 0 && p.zfirst == 0 && part == 0)
         raise_status(p.status, SBL_STATUS_BAD_TARGET);
-      if (p.planes > 1)
-        dz_tile<2>(p, t_acc, row0, n0, lane, box, part, parts, target, live);
-      else
-        dz_tile<1>(p, t_acc, row0, n0, lane, box, part, parts, target, live);
+      dz_tile(p, t_acc, row0, n0, lane, box, part, parts, target, live);
       return;
     }
-    float factor = 0.0f;
-    if (dw)
-      factor = p.planes == 1 && p.dloss_stride == 0 ? __ldcg(p.dloss) : 1.0f;
-    else if (live)
-      factor = p.planes > 1 ? 1.0f : __ldcg(p.dloss + row * p.dloss_stride);
 #pragma unroll 1
     for (int c = part; c < BN / 64; c += parts, turn ^= 4096) {
       const int col0 = n0 + c * 64;
@@ -456,7 +428,7 @@ struct CfgCeBwd {
         const bool none = !dw && !live;  // a row without loss: zero whatever its sums are (NaN weights)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const uint32_t u = pack_bf16(__uint_as_float(r[2 * e]) * factor, __uint_as_float(r[2 * e + 1]) * factor);
+          const uint32_t u = pack_bf16(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
           word[16 * h + e] = none ? 0u : u;
         }
       }
@@ -469,19 +441,17 @@ struct CfgCeBwd {
     return *reinterpret_cast<const uint32_t*>(&h2);
   }
 
-  // dz's tile.  One plane: two boxes in turn, as above.  Two: one box holds the
-  // rounded values, the other what they left.
-  template <int PLANES>
+  // dz's tile: of the two boxes one holds the rounded values, the other what they left.
   __device__ static __forceinline__ void dz_tile(const Params& p, uint32_t t_acc, int row0, int n0, int lane,
                                                  uint8_t* box, int part, int parts, int64_t target, bool live) {
     const int row = row0 + lane;
     const float lse = live ? __ldcg(p.lse + row) : 0.0f;
-    const float factor = PLANES > 1 && live ? __ldcg(p.dloss + row * p.dloss_stride) : 1.0f;
+    const float factor = live ? __ldcg(p.dloss + row * p.dloss_stride) : 0.0f;
 #pragma unroll 1
     for (int c = part; c < BN / 64; c += parts) {
       const int col0 = n0 + c * 64;
       if (col0 >= p.zv) break;  // uniform across the warp
-      if (lane == 0) bulk_store_wait_read<PLANES == 1 ? 1 : 0>();
+      if (lane == 0) bulk_store_wait_read<0>();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t r[32];
@@ -494,8 +464,7 @@ struct CfgCeBwd {
         for (int e = 0; e < 32; ++e) {
           float x = exp_of(__uint_as_float(r[e]) - lse);
           if (at == e) x -= 1.0f;
-          // columns past the piece: beside a second plane they are read as part of its last block
-          const bool none = PLANES > 1 ? !live || e >= left : !live;
+          const bool none = !live || e >= left;  // columns past the piece are read as part of its last block
           r[e] = none ? 0u : __float_as_uint(x * factor);
         }
 #pragma unroll
@@ -505,29 +474,25 @@ struct CfgCeBwd {
           for (int e = 0; e < 4; ++e) {
             const float x = __uint_as_float(r[8 * q + 2 * e]), y = __uint_as_float(r[8 * q + 2 * e + 1]);
             u[e] = pack_bf16(x, y);
-            if constexpr (PLANES > 1)
-              v[e] = pack_bf16(x - __uint_as_float(u[e] << 16), y - __uint_as_float(u[e] & 0xFFFF0000u));
+            v[e] = pack_bf16(x - __uint_as_float(u[e] << 16), y - __uint_as_float(u[e] & 0xFFFF0000u));
           }
           uint8_t* dst = box + lane * 128 + (((4 * h + q) ^ (lane & 7)) << 4);
           *reinterpret_cast<uint4*>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
-          if constexpr (PLANES > 1) *reinterpret_cast<uint4*>(dst + 4096) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(dst + 4096) = make_uint4(v[0], v[1], v[2], v[3]);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         tma_store_2d(&p.dz_out, box, col0, row0);
-        if constexpr (PLANES > 1) tma_store_2d(&p.dz_out, box + 4096, col0 + p.lo, row0);
+        tma_store_2d(&p.dz_out, box + 4096, col0 + p.lo, row0);
         bulk_store_commit();
       }
-      if constexpr (PLANES == 1) box = (c - part) / parts & 1 ? box - 4096 : box + 4096;
     }
   }
 };
 
-// The slices of dh and of dw added in their order, 4 elements a thread.  dh's rows
-// are multiplied by their dloss (dloss NULL: dz held it), dw by the one dloss there
-// is for all rows (dw_factor; NULL: 1).
+// The slices of dh and of dw added in their order, 4 elements a thread.
 struct CeSum {
   const float4* part;  // [slices][slice_n4]
   int slices;
@@ -537,62 +502,57 @@ struct CeSum {
 
 __global__ void __launch_bounds__(256)
     k_ce_sum(const CeSum dh, const CeSum dw, unsigned dh_blocks, int row_n4, const int64_t* __restrict__ targets,
-             const float* __restrict__ dloss, int64_t dloss_stride, const float* __restrict__ dw_factor, int64_t v,
-             int64_t ignore) {
+             int64_t v, int64_t ignore) {
   pdl_wait();
   pdl_trigger();
   const bool first = blockIdx.x < dh_blocks;
   const CeSum& s = first ? dh : dw;
   const int64_t i = int64_t(blockIdx.x - (first ? 0u : dh_blocks)) * 256 + threadIdx.x;
   if (i >= s.n4) return;
-  float g = 1.0f;
   bool live = true;
   if (first) {
-    const int64_t row = i / row_n4, target = targets[row];
+    const int64_t target = targets[i / row_n4];
     live = target >= 0 && target < v && target != ignore;
-    if (live && dloss != nullptr) g = dloss[row * dloss_stride];
-  } else if (dw_factor != nullptr) {
-    g = *dw_factor;
   }
   float4 a = __ldcg(s.part + i);
   for (int k = 1; k < s.slices; ++k) {
     const float4 b = __ldcg(s.part + k * s.slice_n4 + i);
     a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
   }
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * g, a.y * g), hi = __floats2bfloat162_rn(a.z * g, a.w * g);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
   s.out[i] = live ? make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi))
                   : make_uint2(0u, 0u);
 }
 
 // How the backward pass cuts its work.
-constexpr int64_t kCeDzBytes = int64_t(64) << 20;  // dz of one piece: half of L2
+constexpr int64_t kCeDzBytes = int64_t(64) << 20;  // dz of one piece of several: half of L2
 
 struct CePlan {
-  int planes;       // numbers that a dz is the sum of
   int64_t piece;    // vocabulary entries of a piece, a multiple of 256
   int64_t pieces;
   int slices, k_run, dw_slices, dw_run;
   int64_t acc_rows, dw_rows;  // rows of a slice of the sums: t and v up to a multiple of the 32 that a store writes
-  uint64_t dz_bytes, acc_bytes, dw_bytes, scaled_bytes;  // dz: one buffer of two (one piece: of one)
-  uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + dw_bytes + scaled_bytes; }
+  uint64_t dz_bytes, acc_bytes, dw_bytes, live_h_bytes;  // dz: one buffer of two (one piece: of one)
+  uint64_t total() const { return dz_bytes * (pieces > 1 ? 2 : 1) + acc_bytes + dw_bytes + live_h_bytes; }
 };
 
 CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   CePlan c;
   const int64_t padded = (v + 255) / 256 * 256;
-  c.planes = v < kCeWideV ? 2 : 1;
-  const int64_t most = std::max<int64_t>(kCeDzBytes / (2 * c.planes * t) / 256, 1) * 256;
+  // one piece needs one buffer: it may be as large as the two of several
+  const int64_t bytes = t * padded * 4 <= 2 * kCeDzBytes ? 2 * kCeDzBytes : kCeDzBytes;
+  const int64_t most = std::max<int64_t>(bytes / (4 * t) / 256, 1) * 256;
   c.pieces = (padded + most - 1) / most;
   c.piece = ((padded / 256 + c.pieces - 1) / c.pieces) * 256;  // even pieces
   c.pieces = (padded + c.piece - 1) / c.piece;
-  c.dz_bytes = align_up(uint64_t(t) * uint64_t(c.piece) * 2 * c.planes, 256);
-  c.scaled_bytes = align_up(uint64_t(t) * uint64_t(d) * 2, 256);
+  c.dz_bytes = align_up(uint64_t(t) * uint64_t(c.piece) * 4, 256);
+  c.live_h_bytes = align_up(uint64_t(t) * uint64_t(d) * 2, 256);
   // A dh tile is as deep as the piece is wide, a dw tile as there are tokens.  A
   // run of the sum is about what each pair of SMs has to do anyway (or 8 blocks).
   // dw is split where it has few tiles (one piece) and would take twice as long
   // (4096 x 256 x 2560: 69 -> 48 us, 16384 x 256 x 1024: 205 -> 71).
   const int64_t nb = (d + 255) / 256, mb0 = (t + 255) / 256, mb1 = c.piece / 256;
-  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64 * c.planes, kb1 = (t + 63) / 64 * c.planes;
+  const int64_t kb0 = (std::min(c.piece, v) + 63) / 64 * 2, kb1 = (t + 63) / 64 * 2;
   const int64_t pairs = 74;  // 148 SMs
   const int64_t share = std::max<int64_t>((mb0 * nb * kb0 + mb1 * nb * kb1) / pairs, 8);
   int64_t slices = std::min<int64_t>((kb0 + share - 1) / share, 32);
@@ -710,7 +670,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
   ws += c.acc_bytes;
   float* dw_sum = c.dw_bytes ? reinterpret_cast<float*>(ws) : nullptr;
   ws += c.dw_bytes;
-  uint16_t* scaled = reinterpret_cast<uint16_t*>(ws);  // dw's operand
+  uint16_t* live_h = reinterpret_cast<uint16_t*>(ws);  // dw's operand
   cudaError_t e;
   int max_clusters = 0;
   if ((e = pair_setup<CfgCeBwd<4>>(num_sms, &max_clusters)) != cudaSuccess) return e;
@@ -722,8 +682,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
                                            c.dw_slices * c.dw_rows, a.d * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (!rows_map(&dh_out, dh, a.d, a.t, a.d, 32) || !rows_map(&th, h, a.d, a.t, a.d, 64) ||
-      !rows_map(&tw, w, a.d, a.v, a.d, 64) ||
-      !rows_map(&ths, scaled, a.d, a.t, a.d, 64))
+      !rows_map(&tw, w, a.d, a.v, a.d, 64) || !rows_map(&ths, live_h, a.d, a.t, a.d, 64))
     return cudaErrorInvalidValue;
   const auto wide = [&](int64_t i) { return i < 0 || i >= c.pieces ? 0 : std::min(c.piece, a.v - i * c.piece); };
   for (int64_t i = -1; i < c.pieces; ++i) {  // dz of piece i + 1, products of piece i
@@ -734,22 +693,21 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     p.vv = static_cast<int>(wide(i)), p.vfirst = i * c.piece;
     p.targets = a.targets, p.v_all = a.v, p.ignore = a.ignore_index;
     p.lse = a.lse, p.dloss = a.dloss, p.dloss_stride = a.dloss_stride;
-    p.planes = c.planes, p.lo = static_cast<int>(c.piece);
+    p.lo = static_cast<int>(c.piece);
     p.k_run = c.k_run, p.dw_slices = c.dw_slices, p.dw_run = c.dw_run;
     p.slices = (Cfg::depth_dh(p) + c.k_run - 1) / c.k_run;
     p.acc = acc;
     p.add = i > 0;
     p.last = c.slices == 1 && i == c.pieces - 1;
-    p.h = h, p.scaled = i < 0 ? scaled : nullptr;
-    p.row_factor = a.dloss_stride != 0 && c.planes == 1;  // else dz holds dloss, or it multiplies the sums
+    p.h = h, p.live_h = i < 0 ? live_h : nullptr;
     p.status = a.status_dev;
     CUtensorMap tz = th;
     p.dz_out = p.dw_out = p.acc_out = p.dw_sum_out = p.dh_out = dh_out;
-    const auto dz_map = [&](CUtensorMap* map, int64_t j, int64_t cols, int box_rows) {
-      return rows_map(map, dz[j & 1], c.planes > 1 ? 2 * c.piece : cols, a.t, c.planes * c.piece, box_rows);
+    const auto dz_map = [&](CUtensorMap* map, int64_t j, int box_rows) {
+      return rows_map(map, dz[j & 1], 2 * c.piece, a.t, 2 * c.piece, box_rows);
     };
-    if (p.zv > 0 && !dz_map(&p.dz_out, i + 1, p.zv, 32)) return cudaErrorInvalidValue;
-    if (p.vv > 0 && (!dz_map(&tz, i, p.vv, 64) ||
+    if (p.zv > 0 && !dz_map(&p.dz_out, i + 1, 32)) return cudaErrorInvalidValue;
+    if (p.vv > 0 && (!dz_map(&tz, i, 64) ||
                      !rows_map(&p.dw_out, dw + p.vfirst * a.d, a.d, p.vv, a.d, 32)))
       return cudaErrorInvalidValue;
     if (acc != nullptr) p.acc_out = acc_out;
@@ -776,8 +734,7 @@ cudaError_t launch_linear_ce_bwd(const sbl_linear_ce_backward_args& a, int num_s
     const unsigned h_blocks = static_cast<unsigned>((h_sum.n4 + 255) / 256),
                    w_blocks = static_cast<unsigned>((w_sum.n4 + 255) / 256);
     return launch_pdl(k_ce_sum, dim3(h_blocks + w_blocks), dim3(256), 0, s, h_sum, w_sum, h_blocks,
-                      static_cast<int>(a.d / 4), a.targets, c.planes > 1 ? nullptr : a.dloss, a.dloss_stride,
-                      c.planes == 1 && a.dloss_stride == 0 ? a.dloss : nullptr, a.v, a.ignore_index);
+                      static_cast<int>(a.d / 4), a.targets, a.v, a.ignore_index);
   }
   return cudaSuccess;
 }
