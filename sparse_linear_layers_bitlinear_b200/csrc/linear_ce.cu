@@ -526,6 +526,11 @@ __global__ void __launch_bounds__(256)
 
 // How the backward pass cuts its work.
 constexpr int64_t kCeDzBytes = int64_t(64) << 20;  // dz of one piece of several: half of L2
+// A piece's least width, which counts above 8192 tokens: dh's sums (4 t d bytes, past
+// L2 there) are read and written once a piece, so narrow pieces cost more than a dz
+// that leaves L2.  256, 1024, 2048 and 4096 entries: 32768 x 151936 x 3584 198, 180, 170
+// and 171 ms; 32768 x 32768 x 2560 30.7, 25.7, 24.1, 24.9; 131072 x 32768 x 1024 184, 69, 51, 47.
+constexpr int64_t kCeMinPiece = 2048;
 
 struct CePlan {
   int64_t piece;    // vocabulary entries of a piece, a multiple of 256
@@ -541,7 +546,7 @@ CePlan ce_plan(int64_t t, int64_t v, int64_t d) {
   const int64_t padded = (v + 255) / 256 * 256;
   // one piece needs one buffer: it may be as large as the two of several
   const int64_t bytes = t * padded * 4 <= 2 * kCeDzBytes ? 2 * kCeDzBytes : kCeDzBytes;
-  const int64_t most = std::max<int64_t>(bytes / (4 * t) / 256, 1) * 256;
+  const int64_t most = std::max(bytes / (4 * t) / 256 * 256, kCeMinPiece);
   c.pieces = (padded + most - 1) / most;
   c.piece = ((padded / 256 + c.pieces - 1) / c.pieces) * 256;  // even pieces
   c.pieces = (padded + c.piece - 1) / c.piece;

@@ -71,3 +71,16 @@ def test_one_gradient_for_no_rows():
         for value in (float("inf"), float("nan")):
             dh, dw = ce_backward(h, w, y, lse, torch.tensor([value], device="cuda"))
             assert not dh.any() and not dw.any()
+
+
+def test_many_tokens_keep_their_pieces_wide():
+    """dh's sums pass through memory once a piece of the vocabulary: at least 2048 entries each, however many tokens."""
+    t, v, d = 40000, 4500, 64
+    h, w, y = ce_inputs(t, v, d, 4)
+    loss, lse = ce_forward(h, w, y)
+    dloss = randn(t, seed=9, std=0.3, mean=1.0)
+    launched = sbl.launch_count()
+    dh, dw = ce_backward(h, w, y, lse, dloss)
+    assert sbl.launch_count() - launched <= 5  # three pieces: dz of the first, products of each, and a sum at most
+    for got, (want, tol) in zip((dh, dw), exact_backward(h, w, y, lse, dloss)):
+        assert ((got.double() - want).abs() <= tol + 2.0 ** -8 * (want.abs() + tol)).all()
