@@ -682,7 +682,8 @@ _NM = [(1, 2), (2, 2), (1, 4), (2, 4), (3, 4), (4, 4), (1, 8), (2, 8), (3, 8), (
 
 @st.composite
 def _masked_codes(draw):
-    n, m = draw(st.sampled_from(_NM))
+    # 2:4 in half of the draws: a property of 2:4 alone filters the others out, and few may fail a filter
+    n, m = draw(st.one_of(st.just((2, 4)), st.sampled_from(_NM)))
     rows = draw(st.integers(1, 4))
     k = 64 * draw(st.integers(1, 2))
     seed = draw(st.integers(0, 2**31 - 1))
