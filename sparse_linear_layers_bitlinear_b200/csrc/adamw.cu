@@ -90,21 +90,17 @@ __device__ __forceinline__ AdamStep adam_step(const AdamLaunch& p, bool no_decay
   return s;
 }
 
-// One element; m, v and value are updated.  Returns sqrt(v).  The moments'
-// products and sums are rounded one by one (no fused multiply-add) and the root
-// is the IEEE one: behind them stands the rounding to 8 bits, where one unit in
-// the last place decides between two codes 6 to 12 % apart.  With the roundings
-// pinned, the states are the same on every build and in any plain form.
-__device__ __forceinline__ float adam_element(const AdamStep& s, float grad, float& m, float& v, float& value,
-                                              uint32_t& bad) {
+// One element with fp32 states; m, v and value are updated.  The moments'
+// products and sums are rounded one by one (no fused multiply-add): the states are
+// then the same on every build and in any plain form.
+__device__ __forceinline__ void adam_element(const AdamStep& s, float grad, float& m, float& v, float& value,
+                                             uint32_t& bad) {
   const float g = __fmul_rn(grad, s.scale);
   bad = max(bad, __float_as_uint(g) & 0x7FFFFFFFu);
   m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.one_b1, g));
   v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(__fmul_rn(s.one_b2, g), g));
-  const float root = __fsqrt_rn(v);
   // the quotient is off by two units at most; nothing rounds behind it
-  value = fmaf(value, s.keep, -__fdividef(s.rate * m, fmaf(root, s.inv_root, s.eps)));
-  return root;
+  value = fmaf(value, s.keep, -__fdividef(s.rate * m, fmaf(__fsqrt_rn(v), s.inv_root, s.eps)));
 }
 
 template <bool F32>
@@ -156,8 +152,7 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
   return y;
 }
 
-// The sum of two rounded products.  Scalar additions: a packed one behind a
-// packed product was seen to become one fused multiply-add, with one rounding less.
+// The sum of two rounded products, by scalar additions (see f32x2.cuh).
 __device__ __forceinline__ f32x2 sum_of_products(f32x2 a, f32x2 b) {
   const float2 p = halves(a), q = halves(b);
   return pair(__fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y));
@@ -167,7 +162,8 @@ __device__ __forceinline__ f32x2 sum_of_products(f32x2 a, f32x2 b) {
 // y near 1 / sqrt(v) (Markstein, IBM J. Res. Dev. 1990): r = g + (v - g^2) y / 2,
 // the residual exact in a fused multiply-add.  The result before its rounding
 // is within 2^-44 (relative), so it is the rounded root but for about one value
-// in two million, there its neighbour.
+// in two million, there its neighbour: a second moment's code differs from that of
+// the rounded root only where such a value also lies next to a border of two codes.
 __device__ __forceinline__ f32x2 root2(f32x2 v) {
   const float2 f = halves(v);
   const f32x2 y = pair(rsqrt_fast(f.x), rsqrt_fast(f.y));
@@ -218,7 +214,12 @@ __device__ __forceinline__ float warp_top(float top) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
 }
 
-// A block of 256 elements by one warp, 8 consecutive ones a lane, in pairs.
+// A block of 256 elements by one warp, 8 consecutive ones a lane, in pairs.  Behind
+// the moments stands the rounding to 8 bits, where one unit in the last place
+// decides between two codes 6 to 12 % apart: so their products and sums are
+// rounded one by one here too, and the largest value's root, which gives the scale,
+// is the IEEE one.  First moments and both scales are those of any plain form;
+// second moments' codes are but for root2's neighbours.
 template <bool GF32, bool MASTER>
 __device__ __forceinline__ void update_fp8(const AdamEntry& t, const AdamStep& s, int64_t first, uint32_t& bad) {
   const int lane = threadIdx.x & 31;

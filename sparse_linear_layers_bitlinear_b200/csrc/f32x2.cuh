@@ -1,5 +1,7 @@
 // Packed fp32 arithmetic of sm_100: two values in a register pair, each half
-// rounded as the scalar instruction rounds it.
+// rounded as the scalar instruction rounds it.  One exception: results showed that
+// add2 behind mul2 can come out as one fused multiply-add, with one rounding
+// less.  Where both roundings count, take the sum of the halves by __fadd_rn.
 #pragma once
 
 namespace sbl {

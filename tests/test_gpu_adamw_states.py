@@ -1,0 +1,59 @@
+"""AdamW: the 8-bit states against a plain fp32 form bit for bit, and the root that the update divides by."""
+import pytest
+import torch
+
+from sparse_linear_layers_bitlinear_b200 import sbl
+from tests.test_gpu_train_ops import BF, F32, U, randn, same_bits
+
+pytestmark = pytest.mark.gpu
+BLOCK = sbl.SBL_ADAMW_BLOCK
+
+
+def plain_codes(x, top, positive):
+    """Codes of fp32 magnitudes as documented: 448 times the reciprocal of the largest, nearest; no zero of a positive."""
+    q = x * (448.0 * top.reciprocal()).repeat_interleave(BLOCK)
+    if positive:
+        q = torch.where(q > 0, q.clamp_min(2.0 ** -9), q)
+    return q.to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+@pytest.mark.parametrize("spread", [1.0, 6.0])
+def test_8_bit_states_equal_a_plain_form(spread):
+    """First moments and both scales bit for bit.  A second moment's code may be that of the root's neighbour in
+    fp32, which is another one only next to a border of two codes."""
+    n, b1, b2 = 1 << 20, 0.9, 0.95
+    w = randn(n, seed=1, std=0.02, dtype=BF)
+    # gradients over many magnitudes: with the wide spread roots of fewer bits than the smallest code are among them
+    grad = randn(n, seed=2) * (randn(n, seed=3) * spread).exp()
+    t = sbl.AdamWTensor.allocate(w, grad, bits=8)
+    plan = sbl.AdamWTensors([t])
+    for step in (1, 2, 3):
+        m0 = t.m.float() * t.m_scale.repeat_interleave(BLOCK)
+        v0 = t.v.float() * t.v_scale.repeat_interleave(BLOCK)
+        grad.mul_(0.7)
+        f = [torch.tensor(x, dtype=F32, device="cuda") for x in (b1, 1 - b1, b2, 1 - b2)]
+        m = f[0] * m0 + f[1] * grad
+        v = f[2] * (v0 * v0) + f[3] * grad * grad
+        root = v.sqrt()
+        mtop, rtop = m.abs().view(-1, BLOCK).amax(1), root.view(-1, BLOCK).amax(1)
+        sbl.adamw_step(plan, step, lr=1e-3, beta1=b1, beta2=b2)
+        unit = torch.tensor(1 / 448, dtype=F32, device="cuda")
+        assert same_bits(t.m_scale, mtop * unit) and same_bits(t.v_scale, rtop * unit)
+        assert torch.equal(t.m.view(torch.uint8), plain_codes(m, mtop, False))
+        got = t.v.view(torch.uint8)
+        near = [plain_codes(r, rtop, True) for r in (root, torch.nextafter(root, root * 2), torch.nextafter(root, root * 0))]
+        assert ((got == near[0]) | (got == near[1]) | (got == near[2])).all()
+        # a neighbour in one root of two million, and one code of some 2^19 next to a border
+        assert (got != near[0]).sum().item() <= 1
+
+
+def test_the_update_s_root():
+    """beta1 = beta2 = eps = 0 and w = 0: the update is g / sqrt(g^2), 1 but for the roundings: g^2 half of u (of its
+    root), the root itself one step (2 u), the quotient two steps (4 u)."""
+    n = 1 << 20
+    grad = randn(n, seed=4) * (randn(n, seed=5) * 4).exp()
+    t = sbl.AdamWTensor.allocate(torch.zeros(n, dtype=BF, device="cuda"), grad, bits=8)
+    sbl.adamw_step(sbl.AdamWTensors([t]), 1, lr=1.0, beta1=0.0, beta2=0.0, eps=0.0)
+    live = grad.abs() > 2.0 ** -49  # squares that are normal numbers far inside
+    assert live.sum() > n // 2
+    assert ((t.master.double() + grad.sign().double())[live].abs() <= 6.5 * U).all()
