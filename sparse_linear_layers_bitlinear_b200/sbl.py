@@ -530,7 +530,9 @@ class AdamWTensor:
 
 class AdamWTensors:
     """The tensors of ``adamw_step``, checked once; keeps them alive.  Their
-    addresses stay fixed: build a new one when a tensor is reallocated."""
+    addresses are taken here: a field of an AdamWTensor that is set later, or a
+    tensor whose storage moves, is not seen.  Gradients that are allocated anew
+    each step come in by ``set_grads``; for other tensors build a new one."""
 
     def __init__(self, tensors):
         T, me = _torch_types(), "sbl.AdamWTensors"
@@ -558,6 +560,23 @@ class AdamWTensors:
                     raise SblError(SBL_ERR_INVALID_ARG, f"{me}: 8-bit states without m_scale or v_scale")
                 c.m_scale = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
                 c.v_scale = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
+
+    def set_grads(self, grads):
+        """Other gradients from the next step on, one for each tensor in their order (bf16 or fp32, each of its
+        tensor's length); nothing changes if one of them is refused.  A captured graph goes on reading those it was
+        captured with: keep them for it."""
+        T, me = _torch_types(), "sbl.AdamWTensors.set_grads"
+        grads = list(grads)
+        if len(grads) != self.count:
+            raise SblError(SBL_ERR_INVALID_ARG, f"{me}: {len(grads)} gradients for {self.count} tensors")
+        if any(g is None for g in grads):
+            raise SblError(SBL_ERR_INVALID_ARG, f"{me}: a gradient is missing")
+        at = [_addr(me, "grad", g, T.float, c.numel, self.device) for c, g in zip(self.array, grads)]
+        if any(a % 16 for a in at):
+            raise SblError(SBL_ERR_ALIGN, f"{me}: a gradient is not 16-byte aligned")
+        for c, p, g, a in zip(self.array, self.tensors, grads, at):
+            p.grad, c.grad = g, a
+            c.flags = c.flags & ~SBL_ADAMW_GRAD_F32 | (SBL_ADAMW_GRAD_F32 if g.dtype in T.f32 else 0)
 
 
 def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.95,

@@ -57,3 +57,40 @@ def test_the_update_s_root():
     live = grad.abs() > 2.0 ** -49  # squares that are normal numbers far inside
     assert live.sum() > n // 2
     assert ((t.master.double() + grad.sign().double())[live].abs() <= 6.5 * U).all()
+
+
+def test_gradients_allocated_anew_each_step():
+    """set_grads: the next step reads the new gradients, of another type too; a refused set changes nothing."""
+    sizes = (1000, 0, 257, 4096)
+
+    def tensors():
+        out = []
+        for i, n in enumerate(sizes):
+            w = randn(n, seed=i, std=0.02, dtype=BF)
+            out.append(sbl.AdamWTensor.allocate(w, torch.zeros(n, dtype=BF, device="cuda"), bits=8 if i == 3 else 32))
+        return out
+
+    a, b = tensors(), tensors()
+    plan = sbl.AdamWTensors(a)
+    for step, dtype in ((1, BF), (2, F32), (3, BF)):
+        grads = [randn(n, seed=10 * step + i, std=1e-3, dtype=dtype) for i, n in enumerate(sizes)]
+        plan.set_grads(grads)
+        with pytest.raises(sbl.SblError, match="3 gradients for 4 tensors"):
+            plan.set_grads(grads[:3])
+        with pytest.raises(sbl.SblError, match="missing"):
+            plan.set_grads(grads[:3] + [None])
+        with pytest.raises(sbl.SblError, match="has 4095 elements"):
+            plan.set_grads([g.clone() for g in grads[:3]] + [grads[3][:4095]])
+        with pytest.raises(sbl.SblError, match="float16"):
+            plan.set_grads([g.clone() for g in grads[:3]] + [grads[3].half()])
+        with pytest.raises(sbl.SblError, match="aligned"):
+            plan.set_grads(grads[:3] + [torch.zeros(4097, dtype=dtype, device="cuda")[1:]])
+        with pytest.raises(sbl.SblError, match="on cpu"):
+            plan.set_grads(grads[:3] + [grads[3].cpu()])
+        for t, g in zip(b, grads):
+            t.grad = g
+        sbl.adamw_step(plan, step, lr=1e-3)
+        sbl.adamw_step(sbl.AdamWTensors(b), step, lr=1e-3)
+        for t, u in zip(a, b):
+            assert same_bits(t.w, u.w) and same_bits(t.master, u.master)
+            assert torch.equal(t.m.view(torch.uint8), u.m.view(torch.uint8))
