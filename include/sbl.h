@@ -465,7 +465,11 @@ typedef struct sbl_adamw_params {
  * above zero never becomes zero.  A block whose largest magnitude is below
  * 2^-100 holds zeros with scale 0.  The step itself uses m and v before that
  * rounding.  Nearest rounding moves a code only when its value changes by
- * about 3 to 6 %: use beta2 of 0.95 or so with 8-bit states, not 0.999.
+ * about 3 to 6 % against its block's largest in one step.  A second moment then
+ * rises only for a gradient above 1.5 to 1.9 times its root at beta2 = 0.95, 8 to
+ * 11 times at 0.999, and by itself never falls at either (without a gradient the
+ * root loses 2.5 % a step at 0.95), only with its block's largest: use beta2 of
+ * 0.95 or less with 8-bit states, not 0.999.
  * Zeroed states (scales too) are the start.  Tensors of a call must not share
  * memory (two entries with the same w: SBL_ERR_INVALID_ARG).  Alignment: w,
  * master, grad, m and v 16 bytes, the scales 4.  A gradient that is not finite

@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 from dataclasses import dataclass
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -540,6 +541,7 @@ class AdamWTensors:
         self.count = len(self.tensors)
         self.array = (sbl_adamw_tensor * max(self.count, 1))()
         self.device = -1
+        self.eight = False  # whether a tensor holds 8-bit states
         for c, p in zip(self.array, self.tensors):
             if p.w is None or p.grad is None or p.m is None or p.v is None:
                 raise SblError(SBL_ERR_INVALID_ARG, f"{me}: w, grad, m or v is missing")
@@ -554,6 +556,7 @@ class AdamWTensors:
             c.m = _addr(me, "m", p.m, T.code8 if eight else T.f32, n, dev)
             c.v = _addr(me, "v", p.v, T.code8 if eight else T.f32, n, dev)
             c.master = _addr(me, "master", p.master, T.f32, n, dev)
+            self.eight |= eight
             if eight:
                 blocks = (n + SBL_ADAMW_BLOCK - 1) // SBL_ADAMW_BLOCK
                 if p.m_scale is None or p.v_scale is None:
@@ -584,13 +587,17 @@ def adamw_step(tensors: AdamWTensors, step: int, lr: float, beta1: float = 0.9, 
                status=None, stream=None):
     """sbl_adamw_step: one step (the first is ``step`` 1) on every tensor.
     ``lr_dev`` (fp32), ``step_dev`` (int64) and ``grad_scale_dev`` (fp32) are
-    device scalars that a captured graph reads at each replay, or None."""
+    device scalars that a captured graph reads at each replay, or None.  With
+    8-bit states a ``beta2`` above 0.99 warns: nearest rounding then keeps
+    nearly every second moment where it is (see sbl_adamw_step)."""
     T, me = _torch_types(), "sbl_adamw_step"
     if tensors.count == 0:
         return
     dev = tensors.device
     if dev != T.current_device():
         raise SblError(SBL_ERR_DEVICE, f"{me}: the tensors are not on the current CUDA device")
+    if tensors.eight and beta2 > 0.99:
+        warnings.warn(f"{me}: 8-bit second moments hardly move with beta2 = {beta2}; take 0.95 or less", stacklevel=2)
     params = _ADAMW_PARAMS.pack(lr, beta1, beta2, eps, weight_decay, step, _addr(me, "lr_dev", lr_dev, T.f32, 1, dev),
                                 _addr(me, "step_dev", step_dev, T.i64, 1, dev),
                                 _addr(me, "grad_scale_dev", grad_scale_dev, T.f32, 1, dev))

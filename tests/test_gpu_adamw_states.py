@@ -1,4 +1,6 @@
 """AdamW: the 8-bit states against a plain fp32 form bit for bit, and the root that the update divides by."""
+import warnings
+
 import pytest
 import torch
 
@@ -94,3 +96,32 @@ def test_gradients_allocated_anew_each_step():
         for t, u in zip(a, b):
             assert same_bits(t.w, u.w) and same_bits(t.master, u.master)
             assert torch.equal(t.m.view(torch.uint8), u.m.view(torch.uint8))
+
+
+def test_8_bit_states_say_where_they_cannot_follow():
+    """The documented reach of nearest rounding, and the warning beyond it."""
+    n = BLOCK
+
+    def codes(beta2, ratio):
+        """The second moments' codes before and after a step whose gradients are `ratio` times each one's root; the
+        block's largest stays."""
+        v = torch.linspace(8, 112, n, device="cuda").to(torch.float8_e4m3fn)
+        v[0] = 448.0
+        scale = torch.ones(1, device="cuda")
+        grad = v.float() * ratio
+        grad[0] = 448.0
+        t = sbl.AdamWTensor(torch.zeros(n, dtype=BF, device="cuda"), grad, torch.zeros_like(v), v.clone(), scale.clone(), scale.clone())
+        sbl.adamw_step(sbl.AdamWTensors([t]), 100, lr=1e-3, beta2=beta2)
+        assert abs(t.v_scale.item() - 1) < 1e-6
+        return v.float()[1:], t.v.float()[1:]
+
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        for ratio, moves in ((0.0, False), (1.4, False), (2.0, True)):
+            before, after = codes(0.95, ratio)
+            assert torch.equal(before, after) != moves
+            assert not moves or (after > before).all()
+    with pytest.warns(UserWarning, match="hardly move"):
+        for ratio, moves in ((0.0, False), (8.0, False), (12.0, True)):
+            before, after = codes(0.999, ratio)
+            assert torch.equal(before, after) != moves
