@@ -471,7 +471,8 @@ typedef struct sbl_adamw_params {
  * root loses 2.5 % a step at 0.95), only with its block's largest: use beta2 of
  * 0.95 or less with 8-bit states, not 0.999.
  * Zeroed states (scales too) are the start.  Tensors of a call must not share
- * memory (two entries with the same w: SBL_ERR_INVALID_ARG).  Alignment: w,
+ * memory (two entries with the same w, or one array in two places of an entry:
+ * SBL_ERR_INVALID_ARG); entries may share a gradient.  Alignment: w,
  * master, grad, m and v 16 bytes, the scales 4.  A gradient that is not finite
  * (or, with 8-bit states, whose square is not) raises SBL_STATUS_NONFINITE_G;
  * that element, or its block of 256, is then unspecified.  *step_dev must be 1

@@ -542,6 +542,7 @@ class AdamWTensors:
         self.array = (sbl_adamw_tensor * max(self.count, 1))()
         self.device = -1
         self.eight = False  # whether a tensor holds 8-bit states
+        updated = []
         for c, p in zip(self.array, self.tensors):
             if p.w is None or p.grad is None or p.m is None or p.v is None:
                 raise SblError(SBL_ERR_INVALID_ARG, f"{me}: w, grad, m or v is missing")
@@ -563,6 +564,9 @@ class AdamWTensors:
                     raise SblError(SBL_ERR_INVALID_ARG, f"{me}: 8-bit states without m_scale or v_scale")
                 c.m_scale = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
                 c.v_scale = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
+            updated += [a for a in (c.w, c.m, c.v, c.master, c.m_scale, c.v_scale) if a]
+        if len(set(updated)) != len(updated):
+            raise SblError(SBL_ERR_INVALID_ARG, f"{me}: a tensor that is updated stands in two places")
 
     def set_grads(self, grads):
         """Other gradients from the next step on, one for each tensor in their order (bf16 or fp32, each of its

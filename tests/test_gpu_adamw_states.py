@@ -98,6 +98,22 @@ def test_gradients_allocated_anew_each_step():
             assert torch.equal(t.m.view(torch.uint8), u.m.view(torch.uint8))
 
 
+def test_arrays_in_two_places_are_refused():
+    w, u, grad = (randn(512, seed=i, dtype=BF) for i in range(3))
+    z = torch.zeros(512, device="cuda")
+    with pytest.raises(sbl.SblError, match="two places"):
+        sbl.AdamWTensors([sbl.AdamWTensor(w, grad, z, z)])
+    a, b = sbl.AdamWTensor.allocate(w, grad), sbl.AdamWTensor.allocate(u, grad, bits=8)
+    sbl.AdamWTensors([a, b])  # the gradient is only read
+    with pytest.raises(sbl.SblError, match="two places"):
+        sbl.AdamWTensors([a, sbl.AdamWTensor(u, grad, a.m, z)])
+    with pytest.raises(sbl.SblError, match="two places"):
+        sbl.AdamWTensors([a, sbl.AdamWTensor(w, grad, z, z.clone())])
+    b.m_scale = b.v_scale
+    with pytest.raises(sbl.SblError, match="two places"):
+        sbl.AdamWTensors([b])
+
+
 def test_8_bit_states_say_where_they_cannot_follow():
     """The documented reach of nearest rounding, and the warning beyond it."""
     n = BLOCK
