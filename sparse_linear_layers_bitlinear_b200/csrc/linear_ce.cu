@@ -18,10 +18,11 @@
 // in fp32.  With few tokens dh has few output tiles and a long sum over the
 // vocabulary, with few entries dw a long one over the tokens; they are then split
 // over slices that a last launch joins.
-// Measured, sustained, 4096 x 32768 x 2560: 2.88 ms, 1190 TFLOP/s over the five units
-// of 687 Gflop that dz's two numbers make of the three (the library's product of this
-// size in a run of its own: 0.51 ms); what is over are dz's way through L2, dh's fp32
-// sums and the ends of the launches.
+// Measured, sustained, 4096 x 32768 x 2560: 2.85 ms, 1205 TFLOP/s over the five units
+// of 687 Gflop that dz's two numbers make of the three, 1.10 of five such products of
+// the library (0.52 ms each in the same run).  dh's fp32 sums cost 75 us of it and the
+// exponentials 13 (left out of a copy); the rest that is over are dz's way through L2
+// and the ends of the launches.
 #include <algorithm>
 #include <array>
 #include <functional>
@@ -229,7 +230,7 @@ struct CeBwdParams {
 
 // EPI epilogue warps: 4, or 8 with half of a tile's columns each where no pair of
 // SMs has more than one tile and the epilogue's own time counts (63 x 4099 x 512:
-// 17.1 against 18.4 us; 4 keep a stage more of operands).
+// 18.9 against 20.3 us in a graph; 4 keep a stage more of operands).
 template <int EPI>
 struct CfgCeBwd {
   using Params = CeBwdParams;

@@ -16,8 +16,8 @@
 // Measured: forward 4096 x 2560 (fp32 x, bf16 stream, every output) 21.2 us, 5.4
 // TB/s; 8192 x 6912 in bf16 to codes 52 us, 5.4 TB/s, where the schedulers issue 58 %
 // of the time (18 instructions an element).  Backward 4096 x 2560, three bf16
-// gradients, 27.8 us, 4.5 TB/s (3 us of it the second launch); 8191 x 2560 in fp32
-// 68.6 us, 5.5 TB/s.
+// gradients, 27.8 us call by call and 27.1 in a graph, 4.5 TB/s (3 us of it the second
+// launch); 8191 x 2560 in fp32 68.5 us, 5.5 TB/s; 8192 x 6912 in bf16 75 us.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -412,13 +412,16 @@ cudaError_t pick_norm(const NormParams& p, int num_sms, cudaStream_t s) {
 // Backward: g = sum dy, n = h rstd, c = mean(w g n),
 //   dh = dres + rstd (w g - n c),   dw = sum over rows of g n.
 // A group of warps walks rows with a fixed stride and keeps its columns' share
-// of dw in registers.  Up to five arrays are read for one written, so the
-// loads in flight decide the rate: each thread copies its own vectors of the
-// rows to come into its own slots of shared memory (cp.async, a ring of
-// `depth` rows a group), which costs no registers and needs no barrier, since
-// no other thread reads them.  The groups of a block add their dw in shared
-// memory in a fixed order, one row of partial sums a block goes to the
+// of dw in registers.  Up to five arrays are read for one written: each thread
+// copies its own vectors of the rows to come into its own slots of shared memory
+// (cp.async, a ring of `depth` rows a group), which costs no registers and needs no
+// barrier, since no other thread reads them.  The groups of a block add their dw in
+// shared memory in a fixed order, one row of partial sums a block goes to the
 // workspace, and a second launch adds those, in a fixed order too.
+// What bounds 4096 x 2560 with three gradients is a row's chain: some 980
+// instructions a warp and row on 8 warps an SM, seven rows in turn, the schedulers
+// issuing 33 % of the time, with 200 KB an SM on their way; one row more in the ring
+// gains nothing.  fp32 rows are bound by HBM.
 // ---------------------------------------------------------------------------
 struct NormBwdParams {
   const void* h;
@@ -766,7 +769,8 @@ cudaError_t launch_norm_bwd(const NormBwdParams& p, int blocks, size_t smem, cud
 // 75.5 us, 14 of 2 runs 126).  As many rows at a time as 14 warps hold, with the
 // most of them in the ring, but no more than there are rows for all SMs; one
 // block an SM.  The two warps' registers that are left hold blocks of the second
-// launch, which then start at once (4096 x 2560, three gradients: 28.5 -> 27.0 us).
+// launch, which then start at once (4096 x 2560, three gradients, in a graph: 28.2 ->
+// 27.1 us).
 template <bool HF32, bool DF32>
 cudaError_t pick_norm_bwd(NormBwdParams p, float* dw, int num_sms, cudaStream_t s) {
   constexpr int most_warps = kNormBwdThreads / 32;
