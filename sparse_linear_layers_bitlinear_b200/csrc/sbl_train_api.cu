@@ -111,10 +111,12 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
         return SBL_ERR_INVALID_ARG;
       if (!all_aligned16({t.w, t.master, t.grad, t.m, t.v}) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
         return SBL_ERR_ALIGN;
-      // arrays of one tensor that are all updated (those of two tensors are not looked at beyond w: a call is short)
-      if (t.m == t.v || t.m == t.w || t.v == t.w || (t.master != nullptr && (t.master == t.m || t.master == t.v)))
-        return SBL_ERR_INVALID_ARG;
-      if ((t.flags & SBL_ADAMW_STATE_8BIT) && t.m_scale == t.v_scale) return SBL_ERR_INVALID_ARG;
+      // one array in two places of an entry (between entries only w is looked at: a call is short)
+      const void* arrays[] = {t.w, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale};
+      const int n = (t.flags & SBL_ADAMW_STATE_8BIT) ? 7 : 5;
+      for (int a = 0; a < n; ++a)
+        for (int b = 0; b < a; ++b)
+          if (arrays[a] != nullptr && arrays[a] == arrays[b]) return SBL_ERR_INVALID_ARG;
       ws.push_back(t.w);
     }
     if (ws.empty()) return SBL_OK;

@@ -565,7 +565,8 @@ class AdamWTensors:
                 c.m_scale = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
                 c.v_scale = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
             updated += [a for a in (c.w, c.m, c.v, c.master, c.m_scale, c.v_scale) if a]
-        if len(set(updated)) != len(updated):
+        self.updated = set(updated)
+        if len(self.updated) != len(updated) or not self.updated.isdisjoint(c.grad for c in self.array):
             raise SblError(SBL_ERR_INVALID_ARG, f"{me}: a tensor that is updated stands in two places")
 
     def set_grads(self, grads):
@@ -581,6 +582,8 @@ class AdamWTensors:
         at = [_addr(me, "grad", g, T.float, c.numel, self.device) for c, g in zip(self.array, grads)]
         if any(a % 16 for a in at):
             raise SblError(SBL_ERR_ALIGN, f"{me}: a gradient is not 16-byte aligned")
+        if not self.updated.isdisjoint(at):
+            raise SblError(SBL_ERR_INVALID_ARG, f"{me}: a gradient is a tensor that is updated")
         for c, p, g, a in zip(self.array, self.tensors, grads, at):
             p.grad, c.grad = g, a
             c.flags = c.flags & ~SBL_ADAMW_GRAD_F32 | (SBL_ADAMW_GRAD_F32 if g.dtype in T.f32 else 0)

@@ -8,7 +8,8 @@ DISTINCT = dict(w=A, master=A + 0x1000, grad=A + 0x2000, m=A + 0x3000, v=A + 0x4
 
 
 @pytest.mark.parametrize("same,bits", [(("m", "v"), 32), (("m", "w"), 32), (("v", "w"), 32), (("master", "m"), 32),
-                                       (("master", "v"), 32), (("m_scale", "v_scale"), 8), (("m", "v"), 8)])
+                                       (("master", "v"), 32), (("master", "w"), 32), (("grad", "m"), 32),
+                                       (("grad", "w"), 32), (("m_scale", "master"), 8), (("m_scale", "v_scale"), 8), (("m", "v"), 8)])
 def test_one_array_in_two_places(same, bits):
     build.build()
     arr = (sbl.sbl_adamw_tensor * 1)()

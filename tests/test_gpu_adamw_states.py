@@ -109,6 +109,10 @@ def test_arrays_in_two_places_are_refused():
         sbl.AdamWTensors([a, sbl.AdamWTensor(u, grad, a.m, z)])
     with pytest.raises(sbl.SblError, match="two places"):
         sbl.AdamWTensors([a, sbl.AdamWTensor(w, grad, z, z.clone())])
+    with pytest.raises(sbl.SblError, match="two places"):
+        sbl.AdamWTensors([a, sbl.AdamWTensor(u, w, z, z.clone())])
+    with pytest.raises(sbl.SblError, match="is updated"):
+        sbl.AdamWTensors([a]).set_grads([a.m])
     b.m_scale = b.v_scale
     with pytest.raises(sbl.SblError, match="two places"):
         sbl.AdamWTensors([b])
