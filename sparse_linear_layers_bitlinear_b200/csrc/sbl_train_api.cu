@@ -112,11 +112,14 @@ sbl_status sbl_adamw_step(const sbl_adamw_tensor* tensors, int32_t count, const 
       if (!all_aligned16({t.w, t.master, t.grad, t.m, t.v}) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
         return SBL_ERR_ALIGN;
       // one array in two places of an entry (between entries only w is looked at: a call is short)
-      const void* arrays[] = {t.w, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale};
-      const int n = (t.flags & SBL_ADAMW_STATE_8BIT) ? 7 : 5;
-      for (int a = 0; a < n; ++a)
-        for (int b = 0; b < a; ++b)
-          if (arrays[a] != nullptr && arrays[a] == arrays[b]) return SBL_ERR_INVALID_ARG;
+      if ((t.m == t.v) | (t.m == t.w) | (t.v == t.w) | (t.grad == t.w) | (t.grad == t.m) | (t.grad == t.v) |
+          (t.master == t.w) | (t.master == t.m) | (t.master == t.v) | (t.master == t.grad))
+        return SBL_ERR_INVALID_ARG;
+      if (t.flags & SBL_ADAMW_STATE_8BIT)
+        for (const void* scale : {t.m_scale, t.v_scale})
+          if (t.m_scale == t.v_scale || scale == t.w || scale == t.master || scale == t.grad || scale == t.m ||
+              scale == t.v)
+            return SBL_ERR_INVALID_ARG;
       ws.push_back(t.w);
     }
     if (ws.empty()) return SBL_OK;

@@ -542,7 +542,7 @@ class AdamWTensors:
         self.array = (sbl_adamw_tensor * max(self.count, 1))()
         self.device = -1
         self.eight = False  # whether a tensor holds 8-bit states
-        updated = []
+        updated, grads = [], []
         for c, p in zip(self.array, self.tensors):
             if p.w is None or p.grad is None or p.m is None or p.v is None:
                 raise SblError(SBL_ERR_INVALID_ARG, f"{me}: w, grad, m or v is missing")
@@ -552,21 +552,25 @@ class AdamWTensors:
             eight = p.m.dtype not in T.f32
             c.flags = ((SBL_ADAMW_GRAD_F32 if p.grad.dtype in T.f32 else 0) | (SBL_ADAMW_STATE_8BIT if eight else 0)
                        | (0 if p.decay else SBL_ADAMW_NO_DECAY))
-            c.w = _addr(me, "w", p.w, T.bf16, n, dev)
-            c.grad = _addr(me, "grad", p.grad, T.float, n, dev)
-            c.m = _addr(me, "m", p.m, T.code8 if eight else T.f32, n, dev)
-            c.v = _addr(me, "v", p.v, T.code8 if eight else T.f32, n, dev)
-            c.master = _addr(me, "master", p.master, T.f32, n, dev)
+            state = T.code8 if eight else T.f32
+            c.w = w = _addr(me, "w", p.w, T.bf16, n, dev)
+            c.grad = grad = _addr(me, "grad", p.grad, T.float, n, dev)
+            c.m = m = _addr(me, "m", p.m, state, n, dev)
+            c.v = v = _addr(me, "v", p.v, state, n, dev)
+            c.master = master = _addr(me, "master", p.master, T.f32, n, dev)
+            updated += (w, m, v, master)
+            grads.append(grad)
             self.eight |= eight
             if eight:
                 blocks = (n + SBL_ADAMW_BLOCK - 1) // SBL_ADAMW_BLOCK
                 if p.m_scale is None or p.v_scale is None:
                     raise SblError(SBL_ERR_INVALID_ARG, f"{me}: 8-bit states without m_scale or v_scale")
-                c.m_scale = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
-                c.v_scale = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
-            updated += [a for a in (c.w, c.m, c.v, c.master, c.m_scale, c.v_scale) if a]
+                c.m_scale = ms = _addr(me, "m_scale", p.m_scale, T.f32, blocks, dev)
+                c.v_scale = vs = _addr(me, "v_scale", p.v_scale, T.f32, blocks, dev)
+                updated += (ms, vs)
+        updated = [a for a in updated if a]  # no master, or an empty tensor: 0
         self.updated = set(updated)
-        if len(self.updated) != len(updated) or not self.updated.isdisjoint(c.grad for c in self.array):
+        if len(self.updated) != len(updated) or not self.updated.isdisjoint(grads):
             raise SblError(SBL_ERR_INVALID_ARG, f"{me}: a tensor that is updated stands in two places")
 
     def set_grads(self, grads):
