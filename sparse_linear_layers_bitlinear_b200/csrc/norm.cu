@@ -418,7 +418,7 @@ cudaError_t pick_norm(const NormParams& p, int num_sms, cudaStream_t s) {
 // barrier, since no other thread reads them.  The groups of a block add their dw in
 // shared memory in a fixed order, one row of partial sums a block goes to the
 // workspace, and a second launch adds those, in a fixed order too.
-// What bounds 4096 x 2560 with three gradients is a row's chain: some 980
+// What bounds 4096 x 2560 with three gradients is a row's chain: some 890
 // instructions a warp and row on 8 warps an SM, seven rows in turn, the schedulers
 // issuing 33 % of the time, with 200 KB an SM on their way; one row more in the ring
 // gains nothing.  fp32 rows are bound by HBM.
